@@ -44,6 +44,9 @@ ABI_FUNCTIONS = (
     "moe_ep_direct_dispatch", "moe_ep_direct_return", "moe_ep_direct_down_return", "moe_ep_direct_dispatch_fp8",
     "moe_ep_direct_down_return_fp8", "moe_ep_direct_quantize_h", "moe_ep_direct_plan_dispatch",
     "moe_ep_direct_plan_dispatch_quantize", "moe_ep_unpack_combine", "moe_ep_gather_pack",
+    "moe_dispatch", "moe_grouped_swiglu_checkpoint", "moe_forward_checkpoint", "moe_combine_backward",
+    "moe_grouped_down_backward", "moe_grouped_swiglu_backward", "moe_gather_backward", "moe_grouped_swiglu_wgrad",
+    "moe_grouped_down_wgrad", "moe_backward",
 )
 MOE_STATIC_WS_BYTES = 1 << 20
 
@@ -68,6 +71,14 @@ class MoeForwardFp8Args(ctypes.Structure):
         "x", "w_router", "bias", "wg_q", "wg_scale", "wu_q", "wu_scale", "wd_q", "wd_scale", "logits", "topk_idx",
         "topk_w", "expert_counts", "expert_offsets", "src_token", "dest_row", "x_q", "x_scale")] + [
         ("x_q_per_token", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in ("h", "h_q", "h_scale", "y", "out")]
+
+
+class MoeBackwardArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "dout", "x_perm", "y", "w_gate", "w_up", "w_down", "g_q", "u_q", "scale", "topk_idx", "topk_w", "dest_row")] + [
+        ("rebuild_dispatch", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in (
+            "expert_counts", "expert_offsets", "src_token", "dy", "dg", "du", "h", "dx_perm", "dx", "dtopk_w",
+            "dlogits", "dw_gate", "dw_up", "dw_down")]
 
 
 class MoeWsLayout(ctypes.Structure):
@@ -190,6 +201,26 @@ def load_library(path: str = LIB_PATH):
     lib.moe_ep_direct_plan_dispatch.restype = st
     lib.moe_ep_direct_plan_dispatch_quantize.argtypes = [sp, i32, i32] + [vp] * 12
     lib.moe_ep_direct_plan_dispatch_quantize.restype = st
+    lib.moe_dispatch.argtypes = [sp] + [vp] * 7
+    lib.moe_dispatch.restype = st
+    lib.moe_grouped_swiglu_checkpoint.argtypes = [sp] + [vp] * 9
+    lib.moe_grouped_swiglu_checkpoint.restype = st
+    lib.moe_forward_checkpoint.argtypes = [sp, ctypes.POINTER(MoeForwardArgs)] + [vp] * 5
+    lib.moe_forward_checkpoint.restype = st
+    lib.moe_combine_backward.argtypes = [sp] + [vp] * 9
+    lib.moe_combine_backward.restype = st
+    lib.moe_grouped_down_backward.argtypes = [sp] + [vp] * 10
+    lib.moe_grouped_down_backward.restype = st
+    lib.moe_grouped_swiglu_backward.argtypes = [sp] + [vp] * 7
+    lib.moe_grouped_swiglu_backward.restype = st
+    lib.moe_gather_backward.argtypes = [sp] + [vp] * 4
+    lib.moe_gather_backward.restype = st
+    lib.moe_grouped_swiglu_wgrad.argtypes = [sp] + [vp] * 7
+    lib.moe_grouped_swiglu_wgrad.restype = st
+    lib.moe_grouped_down_wgrad.argtypes = [sp] + [vp] * 5
+    lib.moe_grouped_down_wgrad.restype = st
+    lib.moe_backward.argtypes = [sp, ctypes.POINTER(MoeBackwardArgs), vp, vp]
+    lib.moe_backward.restype = st
     _lib = lib
     return lib
 
@@ -460,6 +491,120 @@ def quantize_layer_weights_fp8(shape, bufs, stream=None):
     moe_quantize_weights_fp8(shape, MOE_WEIGHTS_GATE_UP, bufs["w_gate"], bufs["wg_q"], bufs["wg_scale"], stream)
     moe_quantize_weights_fp8(shape, MOE_WEIGHTS_GATE_UP, bufs["w_up"], bufs["wu_q"], bufs["wu_scale"], stream)
     moe_quantize_weights_fp8(shape, MOE_WEIGHTS_DOWN, bufs["w_down"], bufs["wd_q"], bufs["wd_scale"], stream)
+
+
+# ------------------------------------------------------------------ training --
+
+def moe_dispatch(shape, topk_idx, expert_counts, expert_offsets, src_token, dest_row, ws, stream=None):
+    """The index part of moe_permute: rebuilds the schedule in `ws` from topk_idx."""
+    _check(load_library().moe_dispatch(ctypes.byref(shape), _ptr(topk_idx), _ptr(expert_counts), _ptr(expert_offsets),
+                                       _ptr(src_token), _ptr(dest_row), _ptr(ws), _stream(stream)), "moe_dispatch")
+
+
+def moe_grouped_swiglu_checkpoint(shape, x_perm, w_gate, w_up, h, g_q, u_q, scale, ws, stream=None):
+    """moe_grouped_swiglu, also writing the 8-bit checkpoint of gate and up."""
+    _check(load_library().moe_grouped_swiglu_checkpoint(ctypes.byref(shape), _ptr(x_perm), _ptr(w_gate), _ptr(w_up),
+                                                        _ptr(h), _ptr(g_q), _ptr(u_q), _ptr(scale), _ptr(ws),
+                                                        _stream(stream)), "moe_grouped_swiglu_checkpoint")
+
+
+def moe_forward_checkpoint(shape, bufs: dict, ws, stream=None, args: MoeForwardArgs | None = None):
+    """moe_forward keeping the checkpoint in bufs["g_q"], ["u_q"], ["scale"]."""
+    a = args if args is not None else forward_args(bufs)
+    _check(load_library().moe_forward_checkpoint(ctypes.byref(shape), ctypes.byref(a), _ptr(bufs["g_q"]),
+                                                 _ptr(bufs["u_q"]), _ptr(bufs["scale"]), _ptr(ws), _stream(stream)),
+           "moe_forward_checkpoint")
+
+
+def moe_combine_backward(shape, dout, y, dest_row, topk_w, topk_idx, dy, dtopk_w, dlogits=None, stream=None):
+    _check(load_library().moe_combine_backward(ctypes.byref(shape), _ptr(dout), _ptr(y), _ptr(dest_row), _ptr(topk_w),
+                                               _ptr(topk_idx), _ptr(dy), _ptr(dtopk_w), _ptr(dlogits),
+                                               _stream(stream)), "moe_combine_backward")
+
+
+def moe_grouped_down_backward(shape, dy, w_down, g_q, u_q, scale, dg, du, h, ws, stream=None):
+    _check(load_library().moe_grouped_down_backward(ctypes.byref(shape), _ptr(dy), _ptr(w_down), _ptr(g_q), _ptr(u_q),
+                                                    _ptr(scale), _ptr(dg), _ptr(du), _ptr(h), _ptr(ws),
+                                                    _stream(stream)), "moe_grouped_down_backward")
+
+
+def moe_grouped_swiglu_backward(shape, dg, du, w_gate, w_up, dx_perm, ws, stream=None):
+    _check(load_library().moe_grouped_swiglu_backward(ctypes.byref(shape), _ptr(dg), _ptr(du), _ptr(w_gate),
+                                                      _ptr(w_up), _ptr(dx_perm), _ptr(ws), _stream(stream)),
+           "moe_grouped_swiglu_backward")
+
+
+def moe_gather_backward(shape, dx_perm, dest_row, dx, stream=None):
+    _check(load_library().moe_gather_backward(ctypes.byref(shape), _ptr(dx_perm), _ptr(dest_row), _ptr(dx),
+                                              _stream(stream)), "moe_gather_backward")
+
+
+def moe_grouped_swiglu_wgrad(shape, x_perm, dg, du, dw_gate, dw_up, ws, stream=None):
+    _check(load_library().moe_grouped_swiglu_wgrad(ctypes.byref(shape), _ptr(x_perm), _ptr(dg), _ptr(du),
+                                                   _ptr(dw_gate), _ptr(dw_up), _ptr(ws), _stream(stream)),
+           "moe_grouped_swiglu_wgrad")
+
+
+def moe_grouped_down_wgrad(shape, h, dy, dw_down, ws, stream=None):
+    _check(load_library().moe_grouped_down_wgrad(ctypes.byref(shape), _ptr(h), _ptr(dy), _ptr(dw_down), _ptr(ws),
+                                                 _stream(stream)), "moe_grouped_down_wgrad")
+
+
+def backward_args(bufs: dict, rebuild_dispatch=False) -> MoeBackwardArgs:
+    a = MoeBackwardArgs()
+    for name, _ in MoeBackwardArgs._fields_:
+        if name != "rebuild_dispatch":
+            setattr(a, name, _ptr(bufs.get(name)))
+    a.rebuild_dispatch = 1 if rebuild_dispatch else 0
+    return a
+
+
+def moe_backward(shape, bufs: dict, ws, stream=None, args: MoeBackwardArgs | None = None, rebuild_dispatch=False):
+    """bufs: dict with the moe_backward_args field names -> tensors (or None)."""
+    a = args if args is not None else backward_args(bufs, rebuild_dispatch)
+    _check(load_library().moe_backward(ctypes.byref(shape), ctypes.byref(a), _ptr(ws), _stream(stream)),
+           "moe_backward")
+
+
+def alloc_checkpoint(shape: MoeShape, device="cuda"):
+    """The 8-bit checkpoint of one layer: codes of gate and up and their
+    scales (a little over a third of the bytes of g, u and h in bf16)."""
+    import torch
+    P, F = moe_permuted_rows(shape), shape.F
+    if P < 0:
+        raise MoeError("unsupported shape %r" % (shape,))
+    u8 = dict(dtype=torch.uint8, device=torch.device(device))
+    return dict(g_q=torch.empty((P, F), **u8), u_q=torch.empty((P, F), **u8),
+                scale=torch.empty((P, F // 32, 2), **u8))
+
+
+def alloc_backward_buffers(shape: MoeShape, device="cuda"):
+    """Intermediates and results of moe_backward (dx_perm shares dy's memory).
+    h is the forward buffer's name too: pass either."""
+    import torch
+    T, H, F, E, k = shape.T, shape.H, shape.F, shape.E, shape.k
+    P = moe_permuted_rows(shape)
+    if P < 0:
+        raise MoeError("unsupported shape %r" % (shape,))
+    dev = torch.device(device)
+    bf = lambda *n: torch.empty(n, dtype=torch.bfloat16, device=dev)  # noqa: E731
+    b = dict(dy=bf(P, H), dg=bf(P, F), du=bf(P, F), h=bf(P, F), dx=bf(T, H),
+             dtopk_w=torch.empty((T, k), dtype=torch.float32, device=dev),
+             dlogits=torch.empty((T, E), dtype=torch.float32, device=dev),
+             dw_gate=bf(E, H, F), dw_up=bf(E, H, F), dw_down=bf(E, F, H))
+    b["dx_perm"] = b["dy"]
+    return b
+
+
+def checkpoint_values(codes, scale, which):
+    """The values the codes stand for, as fp32: codes [P,F] and scale
+    [P,F/32,2] as moe_grouped_swiglu_checkpoint leaves them; which = 0 for the
+    gate's codes, 1 for the up projection's."""
+    import torch
+    P, F = codes.shape
+    v = codes.view(torch.float8_e4m3fn).to(torch.float32).view(P, F // 32, 8, 4).transpose(2, 3)
+    s = scale.view(torch.float8_e8m0fnu)[..., which].to(torch.float32)
+    return (v.reshape(P, F // 32, 32) * s[..., None]).reshape(P, F)
 
 
 # ---------------------------------------------------- expert-parallel dispatch --

@@ -17,6 +17,18 @@
 //           (block j of the range to accumulator j mod route_groups) and the
 //           epilogue adds them in fp32 in a fixed order.
 //
+//   mode 3, gradient of the down projection and of the SwiGLU product (no
+//           counterpart on the pages: the chain rule of modes 1 and 0):
+//           dh[r, f] = dy[r] . Wd[e][f, :], kept in fp32; with g, u from the
+//           8-bit checkpoint and s = sigmoid(g):
+//           dg = dh u s (1 + g (1 - s)), du = dh g s, h = g s u (bf16)
+//   mode 4, gradient of the gate+up projections:
+//           dx_perm[r, c] = bf16( dg[r] . Wg[e][c, :] + du[r] . Wu[e][c, :] )
+//           one reduction of length 2F: the K blocks of the gate half, then
+//           those of the up half, into the same accumulator.
+//   Modes 3 and 4 reduce over the weights' contiguous dimension, so their
+//   weight operand is K-major where modes 0-2 have it MN-major.
+//
 // Design (B200 first, not the page's Triton kernel):
 // - Swap-AB.  The MMA computes D[feature, row] = W^T[feature, k] * X^T[k, row]:
 //   the expert weights are the M = 128 operand (MN-major, read straight from
@@ -62,11 +74,11 @@
 // - Every wait is bounded: on expiry the kernel records MOE_DEV_GEMM_TIMEOUT,
 //   tells the other roles to stop, lets in-flight copies and MMAs land, frees
 //   its tensor memory and returns.
-#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cudaTypedefs.h>
+#include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "tmap.cuh"
 
 namespace moe {
 
@@ -140,6 +152,11 @@ struct GemmArgs {
     __nv_bfloat16 *comb_out;
     int *comb_cnt;
     int k;
+    // 8-bit checkpoint of the SwiGLU inputs (written by mode 0 with CKPT, read
+    // by mode 3): e4m3 codes [P][n_out] of gate and up, and per (row, 32
+    // features) one scale byte each, [P][n_out / 32][2]
+    uint8_t *g_q, *u_q, *ck_scale;
+    __nv_bfloat16 *out_du, *out_h;  // mode 3: du and h beside out = dg
 };
 
 // Tensor maps of the token matrix (B operand) with boxes of 16 << i rows x 64
@@ -147,6 +164,20 @@ struct GemmArgs {
 struct RowMaps {
     CUtensorMap m[kRowBoxes];
 };
+// Mode 4 reads two token matrices, dg and du.
+struct RowMapsPair {
+    RowMaps a, b;
+};
+template <int MODE>
+struct TokenMaps {
+    using type = RowMaps;
+};
+template <>
+struct TokenMaps<4> {
+    using type = RowMapsPair;
+};
+__device__ __forceinline__ const RowMaps &maps_half(const RowMaps &m, int) { return m; }
+__device__ __forceinline__ const RowMaps &maps_half(const RowMapsPair &m, int half) { return half ? m.b : m.a; }
 
 // Rows [row0, row0 + n) (n a multiple of 16, <= 256) of the token matrix at
 // K offset kx into consecutive 128-byte shared-memory rows from dst, largest
@@ -218,7 +249,7 @@ __device__ __forceinline__ void decode_unit(int u, const int *gts, const GemmArg
     U.n0p = (U.p0l + 15) & ~15;
     U.N = U.n0p + ((U.p1l + 15) & ~15);
     U.fx = U.fb * fbw;
-    U.nacc = (MODE == 0) ? 2 : ((fbw == 256 && U.fx + 128 < a.n_out) ? 2 : 1);
+    U.nacc = (MODE == 0) ? 2 : ((fbw == 256 && U.fx + 128 < a.n_out) ? 2 : 1);  // mode 3: fbw = 128
     U.valid = (unsigned)U.e < (unsigned)a.E && U.N > 0 && U.N <= trows && U.p0s >= 0 && U.p1s >= 0 &&
               U.p0s + U.p0l <= a.P && U.p1s + U.p1l <= a.P && U.fb < num_fb;
 }
@@ -285,7 +316,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(uint32_t lo, uint32_t hi) {
 template <int MODE>
 __device__ __forceinline__ int tmem_width(const Unit &U) {
     if (MODE == 2) return 256;
-    return MODE == 1 && U.nacc == 1 ? (U.N + 1) / 2 : U.N;
+    return MODE != 0 && U.nacc == 1 ? (U.N + 1) / 2 : U.N;
 }
 
 // Tensor memory is two halves of 256 columns.  A unit with <= 128 rows keeps
@@ -347,6 +378,132 @@ __device__ __forceinline__ void load_row_scales(const GemmArgs &a, const Unit &U
 __device__ __forceinline__ void scale_frag(uint32_t (&r)[16], const float (&fs)[4], const float (&rs)[4]) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * fs[frag_fidx(j)] * rs[frag_ridx(j)]);
+}
+
+// ---- 8-bit checkpoint of the gate and up values --------------------------
+// Blocks of 32 features of one row share a power-of-two scale s = 2^(b - 127),
+// b = max(c + 119, 1) for the smallest integer c with max|v| <= 2^c (the
+// largest finite magnitude), so |v / s| <= 256 is inside e4m3's range; code =
+// the nearest e4m3 value of v / s, ties to even; an infinity is stored as NaN.
+// A block is one tensor-memory lane quarter, and byte 4 (f % 8) + f / 8 of its
+// 32 bytes holds feature f: in the fragment layout above a thread holds the
+// features (lane >> 2) + 8 {0..3} of a row, so its four codes are one 32-bit
+// word and neither the store here nor the load of mode 3 needs a transpose
+// (eight lanes x 4 bytes: one full 32-byte sector per row).
+
+// v, or NaN for an infinity (max(|.|) below then skips it, the code is NaN).
+__device__ __forceinline__ float nan_unless_finite(float v) { return v + (v - v); }
+
+// The exponent field of the smallest power of two >= |v| (0 for 0).
+__device__ __forceinline__ uint32_t ceil_pow2_exp(float mag) { return (__float_as_uint(mag) + 0x7FFFFFu) >> 23; }
+
+// Scale byte of a block from its largest magnitude's exponent field.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t ex) { return ex > 9u ? ex - 8u : 1u; }
+
+__device__ __forceinline__ int frag_reg(int fi, int ri) { return 8 * (fi >> 1) + 4 * (ri >> 1) + 2 * (fi & 1) + (ri & 1); }
+
+__device__ __forceinline__ void store_checkpoint(const GemmArgs &a, const Unit &U, int c0, int fbase, int lane,
+                                                 const uint32_t (&rg)[16], const uint32_t (&ru)[16]) {
+    uint32_t ex[4];  // per row: exponent fields of gate (low half) and up (high half)
+#pragma unroll
+    for (int ri = 0; ri < 4; ++ri) {
+        float mg = 0.0f, mu = 0.0f;
+#pragma unroll
+        for (int fi = 0; fi < 4; ++fi) {
+            mg = fmaxf(mg, fabsf(nan_unless_finite(__uint_as_float(rg[frag_reg(fi, ri)]))));
+            mu = fmaxf(mu, fabsf(nan_unless_finite(__uint_as_float(ru[frag_reg(fi, ri)]))));
+        }
+        ex[ri] = ceil_pow2_exp(mg) | (ceil_pow2_exp(mu) << 16);
+    }
+#pragma unroll
+    for (int ri = 0; ri < 4; ++ri) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) ex[ri] = __vmaxu2(ex[ri], __shfl_xor_sync(0xffffffffu, ex[ri], off));
+        const uint32_t bg = scale_byte(ex[ri] & 0xFFFFu), bu = scale_byte(ex[ri] >> 16);
+        // 1 / s = 2^(127 - b), a normal number for every b in [1, 247]
+        const float ig = __uint_as_float((254u - bg) << 23), iu = __uint_as_float((254u - bu) << 23);
+        const int row = unit_row(U, c0 + frag_row_offset(ri, lane));
+        if (row < 0) continue;
+        float vg[4], vu[4];
+#pragma unroll
+        for (int fi = 0; fi < 4; ++fi) {
+            vg[fi] = nan_unless_finite(__uint_as_float(rg[frag_reg(fi, ri)])) * ig;
+            vu[fi] = nan_unless_finite(__uint_as_float(ru[frag_reg(fi, ri)])) * iu;
+        }
+        const size_t at = (size_t)row * a.n_out + fbase + 4 * (lane >> 2);
+        *reinterpret_cast<uint32_t *>(a.g_q + at) =
+            (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(vg[0], vg[1]), __NV_SATFINITE, __NV_E4M3) |
+            (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(vg[2], vg[3]), __NV_SATFINITE, __NV_E4M3) << 16;
+        *reinterpret_cast<uint32_t *>(a.u_q + at) =
+            (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(vu[0], vu[1]), __NV_SATFINITE, __NV_E4M3) |
+            (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(vu[2], vu[3]), __NV_SATFINITE, __NV_E4M3) << 16;
+        if ((lane >> 2) == ri)  // one lane group per row writes its two scale bytes
+            *reinterpret_cast<uint16_t *>(a.ck_scale + ((size_t)row * (a.n_out / 32) + fbase / 32) * 2) =
+                (uint16_t)(bg | bu << 8);
+    }
+}
+
+__device__ __forceinline__ void unpack_e4m3x4(uint32_t w, float s, float (&v)[4]) {
+    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
+    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    v[0] = a.x * s;
+    v[1] = a.y * s;
+    v[2] = b.x * s;
+    v[3] = b.y * s;
+}
+
+// Mode 3, the 16 rows x 32 features at unit column c0: dh from tensor memory
+// (fp32), gate and up from the checkpoint, dg, du and h stored as bf16 (the
+// gradients' and activations' type; the only roundings).  The sigmoid is
+// 1 / (1 + e^-g) with the fast exponential and division (a few 2^-22), not the
+// tanh of the forward epilogue: far negative g would lose its small value.
+__device__ __forceinline__ void swiglu_backward_chunk(const GemmArgs &a, const Unit &U, uint32_t t0, int c0, int fbase,
+                                                      int lane, uint8_t *stg) {
+    uint32_t wg[4], wu[4], sc[4];
+#pragma unroll
+    for (int ri = 0; ri < 4; ++ri) {
+        const int row = unit_row(U, c0 + frag_row_offset(ri, lane));
+        wg[ri] = wu[ri] = sc[ri] = 0u;
+        if (row >= 0) {
+            const size_t at = (size_t)row * a.n_out + fbase + 4 * (lane >> 2);
+            wg[ri] = __ldg(reinterpret_cast<const uint32_t *>(a.g_q + at));
+            wu[ri] = __ldg(reinterpret_cast<const uint32_t *>(a.u_q + at));
+            sc[ri] = __ldg(reinterpret_cast<const uint16_t *>(a.ck_scale +
+                                                              ((size_t)row * (a.n_out / 32) + fbase / 32) * 2));
+        }
+    }
+    uint32_t r[16];
+    tmem_ld_frag16(t0 + (uint32_t)c0, r);
+    tmem_ld_wait();
+    uint32_t dg[16], du[16], hh[16];
+#pragma unroll
+    for (int ri = 0; ri < 4; ++ri) {
+        float g[4], u[4];
+        unpack_e4m3x4(wg[ri], __uint_as_float((sc[ri] & 0xFFu) << 23), g);
+        unpack_e4m3x4(wu[ri], __uint_as_float((sc[ri] >> 8) << 23), u);
+#pragma unroll
+        for (int fi = 0; fi < 4; ++fi) {
+            const int j = frag_reg(fi, ri);
+            const float dh = __uint_as_float(r[j]);
+            const float s = __fdividef(1.0f, 1.0f + __expf(-g[fi]));
+            const float silu = g[fi] * s;
+            dg[j] = __float_as_uint(dh * u[fi] * fmaf(silu, 1.0f - s, s));
+            du[j] = __float_as_uint(dh * silu);
+            hh[j] = __float_as_uint(silu * u[fi]);
+        }
+    }
+    uint32_t w[8];
+#pragma unroll
+    for (int m = 0; m < 8; ++m) w[m] = pack_bf16x2(dg[2 * m], dg[2 * m + 1]);
+    store_block_frag(w, stg, a.out, a.n_out, nullptr, fbase, U, c0);
+#pragma unroll
+    for (int m = 0; m < 8; ++m) w[m] = pack_bf16x2(du[2 * m], du[2 * m + 1]);
+    store_block_frag(w, stg, a.out_du, a.n_out, nullptr, fbase, U, c0);
+#pragma unroll
+    for (int m = 0; m < 8; ++m) w[m] = pack_bf16x2(hh[2 * m], hh[2 * m + 1]);
+    store_block_frag(w, stg, a.out_h, a.n_out, nullptr, fbase, U, c0);
 }
 
 // Step 5 for one token t and one 128-feature block b, by 16 lanes (lane l of
@@ -475,13 +632,18 @@ __device__ __forceinline__ void raise_abort(volatile int *abort, uint32_t *statu
 // its feature's power-of-two scales (exact) before the bf16 results.
 // COMBINE (mode 1 only): the weighted combine of step 5 in the epilogue (see
 // arrive_and_combine).
-template <int MODE, bool GATHER = false, bool FP8 = false, bool COMBINE = false>
+// CKPT (mode 0 only): the epilogue also writes the 8-bit checkpoint of the
+// gate and up values (see store_checkpoint).
+template <int MODE, bool GATHER = false, bool FP8 = false, bool COMBINE = false, bool CKPT = false>
 __global__ void __launch_bounds__(kThreads, 1)
     k_grouped_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
-                   const __grid_constant__ RowMaps tmB, GemmArgs a) {
+                   const __grid_constant__ typename TokenMaps<MODE>::type tmB, GemmArgs a) {
     static_assert(!GATHER || MODE == 0, "the row gather feeds the SwiGLU GEMM");
     static_assert(!COMBINE || MODE == 1, "the combine follows the down projection");
-    static_assert(!FP8 || MODE != 2, "the router runs on bf16 planes");
+    static_assert(!FP8 || MODE < 2, "only the expert GEMMs of the forward pass run on fp8 operands");
+    static_assert(!CKPT || (MODE == 0 && !FP8), "the checkpoint is taken from the bf16 SwiGLU GEMM");
+    constexpr bool kKMajorA = MODE >= 3;      // bf16 weights with the reduction dimension contiguous
+    constexpr bool kDown = MODE == 1 || MODE == 4;  // plain bf16 results, 128- or 256-feature units
     constexpr int kStageK = FP8 ? 128 : kBK;  // K elements per stage: 128 bytes of each row
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -525,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmA0);
         tma_prefetch_desc(&tmA1);
         for (int b = 0; b < kRowBoxes; ++b)
-            if ((a.row_boxes >> b) & 1u) tma_prefetch_desc(&tmB.m[b]);
+            if ((a.row_boxes >> b) & 1u) tma_prefetch_desc(&maps_half(tmB, 0).m[b]);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, kTmemCols);
@@ -537,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     pdl_wait();  // the schedule and the token rows come from earlier kernels
     int total, trows;
-    int num_fb = a.num_fb, fbw = MODE == 0 ? 128 : 256;
+    int num_fb = a.num_fb, fbw = MODE == 0 || MODE == 3 ? 128 : 256;
     if (MODE == 2) {
         total = (a.T + a.route_rows - 1) / a.route_rows * a.route_q;
         trows = a.route_rows;
@@ -554,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int grid = (int)gridDim.x;
         const int tr = *a.tile_rows;
         const int r256 = (nt * a.num_fb + grid - 1) / grid, r128 = (nt * (a.n_out / 128) + grid - 1) / grid;
-        if (MODE == 1 && r128 * (128 + tr) < r256 * (256 + tr)) {
+        if (kDown && r128 * (128 + tr) < r256 * (256 + tr)) {
             num_fb = a.n_out / 128;
             fbw = 128;
         }
@@ -586,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     trows = trows < 16 ? 16 : (trows > kTileRows ? kTileRows : (trows + 15) & ~15);
     // weight tiles per stage: both accumulators' (gate and up, or two
     // 128-feature blocks), one for 128-feature down units (twice the stages)
-    const uint32_t a_tiles = MODE == 2 ? 3u * (a.E > 128 ? 2u : 1u) : (MODE == 1 && fbw == 128 ? 1u : 2u);
+    const uint32_t a_tiles = MODE == 2 ? 3u * (a.E > 128 ? 2u : 1u) : (MODE != 0 && fbw == 128 ? 1u : 2u);
     const uint32_t a_bytes = a_tiles * kATile, b_bytes = (uint32_t)trows * kBRowBytes;
     int nb = kMaxBStages;
     int fit = (int)((kRingBytes - (uint32_t)nb * b_bytes) / a_bytes);
@@ -652,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint8_t *sb = ringB + stage * b_bytes;
                     const int kx = kb * kStageK;
                     for (int g = 0; g < U.N; g += 4)
-                        tma_gather4(sb + g * kBRowBytes, &tmB.m[0], &fullB[stage], kx, s_rows[g], s_rows[g + 1],
+                        tma_gather4(sb + g * kBRowBytes, &maps_half(tmB, 0).m[0], &fullB[stage], kx, s_rows[g], s_rows[g + 1],
                                     s_rows[g + 2], s_rows[g + 3]);
                     issued_ph[stage] = (int)ph;
                 }
@@ -697,6 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t bytes = is_a ? (MODE == 2 ? 3u : 1u) * (uint32_t)U.nacc * kATile
                                             : (uint32_t)(nb0 + nb1) * kBBox;
                 const int krow = U.e * a.K;
+                const int half = MODE == 4 ? nk / 2 : nk;  // mode 4: K blocks from here on are the up half's
                 const int kb0 = MODE == 2 ? U.fb * a.route_kb : 0;
                 const int kb1 = MODE == 2 ? min(nk, kb0 + a.route_kb) : nk;
                 bool ok = true;
@@ -718,8 +881,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int ky = krow + kb * kBK, kx = kb * kStageK;
                     if (!is_a) {
                         uint8_t *sb = ringB + stage * b_bytes;
-                        tma_load_rows(sb, tmB, a.row_boxes, &full[stage], kx, U.p0s, 16 * nb0);
-                        if (nb1) tma_load_rows(sb + U.n0p * kBRowBytes, tmB, a.row_boxes, &full[stage], kx, U.p1s, 16 * nb1);
+                        const RowMaps &rm = maps_half(tmB, kb >= half);
+                        const int bx = MODE == 4 && kb >= half ? kx - half * kStageK : kx;
+                        tma_load_rows(sb, rm, a.row_boxes, &full[stage], bx, U.p0s, 16 * nb0);
+                        if (nb1) tma_load_rows(sb + U.n0p * kBRowBytes, rm, a.row_boxes, &full[stage], bx, U.p1s, 16 * nb1);
                     } else if (MODE == 2) {
                         // tile (plane p, accumulator c) at index p * nacc + c;
                         // plane p holds rows [p*K, (p+1)*K) of the plane tensor
@@ -742,6 +907,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (U.nacc == 2)
                             tma_load_2d(sa0 + kATile, &tmA1, &full[stage], 0,
                                         ((U.e * nbk + fx1 / 128) * kbk + kx / 128) * 128);
+                    } else if (kKMajorA) {
+                        // rows e * n_out + feature of a [E * n_out, K] weight
+                        // tensor: 128 features x 64 K per accumulator, one box
+                        uint8_t *sa0 = smem + stage * a_bytes;
+                        const bool up = kb >= half;
+                        const CUtensorMap *tm = up ? &tmA1 : &tmA0;
+                        const int ax = up ? kx - half * kStageK : kx;
+                        tma_load_2d(sa0, tm, &full[stage], ax, U.e * a.n_out + fx0);
+                        if (U.nacc == 2) tma_load_2d(sa0 + kATile, tm, &full[stage], ax, U.e * a.n_out + fx1);
                     } else {
                         uint8_t *sa0 = smem + stage * a_bytes, *sa1 = sa0 + kATile;
                         tma_load_2d(sa0, &tmA0, &full[stage], fx0, ky);
@@ -780,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Unit U;
                 decode_unit<MODE>(u, s_gts, a, trows, num_fb, fbw, U);
                 if (!U.valid) continue;
-                const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, U.N) : idesc_bf16_f32(128, U.N, 1, 0);
+                const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, U.N) : idesc_bf16_f32(128, U.N, kKMajorA ? 0 : 1, 0);
                 uint32_t h;
                 bool big;
                 plan.place(tmem_width<MODE>(U), h, big);  // mode 2 uses all of tensor memory
@@ -829,11 +1003,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // B: K-major, 16 K-elements (32 bytes) per MMA inside the 128-byte row.
                         const uint64_t bdesc = sdesc_sw128(sbt + kk * 32, 16, 1024);
                         // A: MN-major, 16 K-rows (2 KiB) per MMA; the two 64-feature halves 8 KiB apart.
-                        const uint64_t a0desc = sdesc_sw128(sa0 + kk * 2048, kABox, 1024);
+                        // K-major A (modes 3, 4): stepped like B.
+                        const uint64_t a0desc =
+                            kKMajorA ? sdesc_sw128(sa0 + kk * 32, 16, 1024) : sdesc_sw128(sa0 + kk * 2048, kABox, 1024);
                         const uint32_t accum = (kb | kk) ? 1u : 0u;
                         tc_mma_bf16(d0, a0desc, bdesc, idesc, accum);
                         if (U.nacc == 2) {
-                            const uint64_t a1desc = sdesc_sw128(sa1 + kk * 2048, kABox, 1024);
+                            const uint64_t a1desc = kKMajorA ? sdesc_sw128(sa1 + kk * 32, 16, 1024)
+                                                             : sdesc_sw128(sa1 + kk * 2048, kABox, 1024);
                             tc_mma_bf16(d1, a1desc, bdesc, idesc, accum);
                         }
                     }
@@ -938,7 +1115,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 plan.advance(big, h);
                 continue;
             }
-            if (MODE == 1 && big) {
+            if (MODE == 3) {
+                // One accumulator of up to 256 columns in one half (its
+                // epilogue overlaps the next unit's MMAs): dh stays in fp32.
+#pragma unroll 1
+                for (int c0 = sub * 16; c0 < U.N; c0 += 16 * kEpiSub)
+                    swiglu_backward_chunk(a, U, t0, c0, U.fx + q * 32, lane, stg);
+                release();
+                plan.advance(big, h);
+                continue;
+            }
+            if (kDown && big) {
                 // Two accumulators of up to 256 columns each: accumulator 0 of
                 // every chunk and accumulator 1 of the first kHold1 chunks go to
                 // registers as packed bf16; the rest of accumulator 1 is stored
@@ -1000,7 +1187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 plan.advance(big, h);
                 continue;
             }
-            if (MODE == 1 && U.nacc == 1) {
+            if (kDown && U.nacc == 1) {
                 // One accumulator of up to 256 columns in one half: up to four
                 // 16-column chunks per warp, packed into registers, then handed
                 // back before the stores.
@@ -1051,6 +1238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         scale_frag(r0, fs0, rs);
                         if (U.nacc == 2) scale_frag(r1, fs1, rs);
                     }
+                    if (CKPT) store_checkpoint(a, U, c0, U.fx + q * 32, lane, r0, r1);
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
                         if (MODE == 0) {
@@ -1082,7 +1270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int m = 0; m < 8; ++m) w[m] = hold[i][m];
                     store_block_frag(w, stg, a.out, a.n_out, a.row_addr, U.fx + q * 32, U, c0);
-                    if (MODE == 1 && U.nacc == 2) {
+                    if (kDown && U.nacc == 2) {
 #pragma unroll
                         for (int m = 0; m < 8; ++m) w[m] = hold[i][8 + m];
                         store_block_frag(w, stg, a.out, a.n_out, a.row_addr, U.fx + 128 + q * 32, U, c0);
@@ -1124,36 +1312,6 @@ __global__ void __launch_bounds__(256) k_router_planes(const float *__restrict__
         planes[n + i] = p1;
         planes[2 * n + i] = __float2bfloat16_rn(r2);
     }
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    return fn;
-}
-
-// 2-D tensor map over a row-major [rows, cols] matrix of bf16 (or, with
-// bytes = true, of 8-bit codes) with the 128-byte swizzle; box = box_cols x
-// box_rows (box_cols elements must span 128 bytes).
-bool make_tmap(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint32_t box_cols,
-               uint32_t box_rows, bool bytes = false) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {cols * (bytes ? 1 : 2)};
-    cuuint32_t box[2] = {box_cols, box_rows};
-    cuuint32_t es[2] = {1, 1};
-    const CUresult r = fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                          const_cast<void *>(ptr), dims, strides, box, es,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
 }
 
 // The token matrix with boxes of 16, 32, ... 256 rows; returns the mask of the
@@ -1301,6 +1459,62 @@ cudaError_t launch_grouped_gemm(int mode, const moe_shape &s, const void *act, c
         if (err != cudaSuccess) return err;
     }
     return cudaGetLastError();
+}
+
+// mode 0 with the 8-bit checkpoint: as launch_grouped_gemm mode 0 on x_perm.
+// mode 3: act = dy [P,H], w0 = down [E,F,H], out = dg, du, h [P,F].
+// mode 4: act = dg, act1 = du [P,F], w0 = gate, w1 = up [E,H,F], out = dx_perm [P,H].
+cudaError_t launch_grouped_gemm_train(int mode, const moe_shape &s, const void *act, const void *act1, const void *w0,
+                                      const void *w1, void *out, void *out_du, void *out_h, const void *g_q,
+                                      const void *u_q, const void *ck_scale, const WsLayout &L, void *ws,
+                                      uint64_t timeout_ns, int num_sms, cudaStream_t stream) {
+    const int64_t P = permuted_rows(s.T, s.E, s.k, s.C, (s.flags & MOE_FLAG_CAPACITY) != 0);
+    const int n_out = mode == 4 ? s.H : s.F;
+    const int width = mode == 4 ? s.F : s.H;  // row length of the token matrices
+    CUtensorMap tA0, tA1;
+    RowMapsPair tB;
+    if (mode == 0) {
+        if (!make_tmap(&tA0, w0, (uint64_t)s.E * s.H, (uint64_t)s.F, 64, 64) ||
+            !make_tmap(&tA1, w1, (uint64_t)s.E * s.H, (uint64_t)s.F, 64, 64))
+            return cudaErrorInvalidValue;
+    } else if (!make_tmap(&tA0, w0, (uint64_t)s.E * n_out, (uint64_t)width, 64, 128) ||
+               !make_tmap(&tA1, w1, (uint64_t)s.E * n_out, (uint64_t)width, 64, 128)) {
+        return cudaErrorInvalidValue;
+    }
+    uint32_t boxes = make_row_maps(&tB.a, act, (uint64_t)P, (uint64_t)width);
+    if (mode == 4) boxes &= make_row_maps(&tB.b, act1, (uint64_t)P, (uint64_t)width);
+    if (!(boxes & 1u)) return cudaErrorInvalidValue;
+    WsPtrs p = ws_ptrs(ws, L);
+    GemmArgs a = {};
+    a.tile_map = p.tile_map;
+    a.grp_tile_start = p.grp_tile_start;
+    a.num_tiles = p.num_tiles;
+    a.tile_rows = p.tile_rows;
+    a.status = p.status;
+    a.out = (__nv_bfloat16 *)out;
+    a.out_du = (__nv_bfloat16 *)out_du;
+    a.out_h = (__nv_bfloat16 *)out_h;
+    a.g_q = (uint8_t *)g_q;
+    a.u_q = (uint8_t *)u_q;
+    a.ck_scale = (uint8_t *)ck_scale;
+    a.n_out = n_out;
+    a.K = mode == 4 ? 2 * s.F : s.H;
+    a.num_fb = mode == 4 ? (s.H + 255) / 256 : s.F / 128;
+    a.E = s.E;
+    a.P = (int)P;
+    a.max_tiles = L.max_tiles;
+    a.timeout_ns = timeout_ns;
+    a.T = s.T;
+    a.row_boxes = boxes;
+    auto go = [&](auto kernel, const auto &tB_) -> cudaError_t {
+        // set on every call: the attribute belongs to the current device
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(kernel, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA0, tA1, tB_, a);
+    };
+    if (mode == 0) return go(k_grouped_gemm<0, false, false, false, true>, tB.a);
+    if (mode == 3) return go(k_grouped_gemm<3>, tB.a);
+    return go(k_grouped_gemm<4>, tB);
 }
 
 // FP8 expert GEMMs.  mode 0: act = the e4m3 token rows (x_perm codes [P,H],

@@ -37,6 +37,18 @@ cudaError_t launch_quant_rows(const moe_shape &s, int K, const void *src, int sr
                               cudaStream_t stream);
 cudaError_t launch_quant_tokens(const moe_shape &s, const void *x, void *q, float *scale, int num_sms,
                                 cudaStream_t stream);
+cudaError_t launch_grouped_gemm_train(int mode, const moe_shape &s, const void *act, const void *act1, const void *w0,
+                                      const void *w1, void *out, void *out_du, void *out_h, const void *g_q,
+                                      const void *u_q, const void *ck_scale, const WsLayout &L, void *ws,
+                                      uint64_t timeout_ns, int num_sms, cudaStream_t stream);
+cudaError_t launch_wgrad(const moe_shape &s, int MA, int NB, const void *A, const void *B0, const void *B1, void *dW0,
+                         void *dW1, const WsLayout &L, void *ws, uint64_t timeout_ns, int num_sms,
+                         cudaStream_t stream);
+cudaError_t launch_combine_backward(const moe_shape &s, const void *dout, const void *y, const int32_t *dest_row,
+                                    const float *topk_w, const int32_t *topk_idx, void *dy, float *dtopk_w,
+                                    float *dlogits, cudaStream_t stream);
+cudaError_t launch_gather_backward(const moe_shape &s, const void *dx_perm, const int32_t *dest_row, void *dx,
+                                   cudaStream_t stream);
 int64_t ep_overflow_rows(const moe_shape &s, int G);
 size_t ep_workspace_bytes(const moe_shape &s, int G);
 cudaError_t launch_ep_pack(const moe_shape &s, int G, const void *x_perm, const WsLayout &L, void *ws, void *send_ovf,
@@ -375,6 +387,188 @@ moe_status moe_forward(const moe_shape *s, const moe_forward_args *a, void *ws, 
     st = moe_grouped_down(s, a->h, a->w_down, a->y, ws, stream);
     if (st != MOE_OK) return st;
     return moe_combine(s, a->y, a->dest_row, a->topk_w, a->out, stream);
+}
+
+// ------------------------------------------------------------- training ----
+
+moe_status moe_dispatch(const moe_shape *s, const int32_t *topk_idx, int32_t *expert_counts, int32_t *expert_offsets,
+                        int32_t *src_token, int32_t *dest_row, void *ws, void *stream) {
+    moe_status st = check_shape(s);
+    if (st != MOE_OK) return st;
+    if (!aligned(topk_idx, 4) || !aligned(expert_counts, 4) || !aligned(expert_offsets, 4) ||
+        !aligned(src_token, 4) || !aligned(dest_row, 4))
+        return MOE_ERR_INVALID_ARG;
+    if ((st = check_ws(ws)) != MOE_OK) return st;
+    int sms = 0;
+    if ((st = device_info(&sms)) != MOE_OK) return st;
+    const WsLayout L = layout_of(s);
+    cudaError_t e = launch_dispatch_index(*s, topk_idx, expert_counts, expert_offsets, src_token, dest_row, L, ws,
+                                          g_timeout_ns.load(), sms, (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_dispatch");
+}
+
+moe_status moe_grouped_swiglu_checkpoint(const moe_shape *s, const void *x_perm, const void *w_gate, const void *w_up,
+                                         void *h, void *g_q, void *u_q, void *scale, void *ws, void *stream) {
+    moe_status st = check_shape(s);
+    if (st != MOE_OK) return st;
+    if (!aligned(x_perm, 16) || !aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(h, 16) || !aligned(g_q, 16) ||
+        !aligned(u_q, 16) || !aligned(scale, 2))
+        return MOE_ERR_INVALID_ARG;
+    if ((st = check_ws(ws)) != MOE_OK) return st;
+    int sms = 0;
+    if ((st = device_info(&sms)) != MOE_OK) return st;
+    const WsLayout L = layout_of(s);
+    cudaError_t e = launch_grouped_gemm_train(0, *s, x_perm, nullptr, w_gate, w_up, h, nullptr, nullptr, g_q, u_q,
+                                              scale, L, ws, g_timeout_ns.load(), sms, (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_grouped_swiglu_checkpoint");
+}
+
+moe_status moe_forward_checkpoint(const moe_shape *s, const moe_forward_args *a, void *g_q, void *u_q, void *scale,
+                                  void *ws, void *stream) {
+    // what the steps would refuse is refused before the first of them is enqueued
+    if (!a || !aligned(a->x_perm, 16) || !aligned(g_q, 16) || !aligned(u_q, 16) || !aligned(scale, 2) ||
+        !aligned(a->w_gate, 16) || !aligned(a->w_up, 16) || !aligned(a->w_down, 16) || !aligned(a->h, 16) ||
+        !aligned(a->y, 16) || !aligned(a->out, 16))
+        return MOE_ERR_INVALID_ARG;
+    moe_status st = moe_route_dispatch(s, a->x, a->w_router, a->bias, a->logits, a->topk_idx, a->topk_w,
+                                       a->expert_counts, a->expert_offsets, a->src_token, a->dest_row, ws, stream);
+    if (st != MOE_OK) return st;
+    if ((st = moe_gather(s, a->x, a->src_token, a->x_perm, ws, stream)) != MOE_OK) return st;
+    st = moe_grouped_swiglu_checkpoint(s, a->x_perm, a->w_gate, a->w_up, a->h, g_q, u_q, scale, ws, stream);
+    if (st != MOE_OK) return st;
+    if (s->flags & MOE_FLAG_FUSED_COMBINE)
+        return moe_grouped_down_combine(s, a->h, a->w_down, a->src_token, a->dest_row, a->topk_w, a->y, a->out, ws,
+                                        stream);
+    if ((st = moe_grouped_down(s, a->h, a->w_down, a->y, ws, stream)) != MOE_OK) return st;
+    return moe_combine(s, a->y, a->dest_row, a->topk_w, a->out, stream);
+}
+
+moe_status moe_combine_backward(const moe_shape *s, const void *dout, const void *y, const int32_t *dest_row,
+                                const float *topk_w, const int32_t *topk_idx, void *dy, float *dtopk_w,
+                                float *dlogits, void *stream) {
+    moe_status st = check_shape(s);
+    if (st != MOE_OK) return st;
+    if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dest_row, 4) || !aligned(topk_w, 4) || !aligned(dy, 16) ||
+        !aligned(dtopk_w, 4) || (dlogits && (!aligned(dlogits, 4) || !aligned(topk_idx, 4))))
+        return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = device_info(&sms)) != MOE_OK) return st;
+    cudaError_t e = launch_combine_backward(*s, dout, y, dest_row, topk_w, topk_idx, dy, dtopk_w, dlogits,
+                                            (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_combine_backward");
+}
+
+moe_status moe_grouped_down_backward(const moe_shape *s, const void *dy, const void *w_down, const void *g_q,
+                                     const void *u_q, const void *scale, void *dg, void *du, void *h, void *ws,
+                                     void *stream) {
+    moe_status st = check_shape(s);
+    if (st != MOE_OK) return st;
+    if (!aligned(dy, 16) || !aligned(w_down, 16) || !aligned(g_q, 16) || !aligned(u_q, 16) || !aligned(scale, 2) ||
+        !aligned(dg, 16) || !aligned(du, 16) || !aligned(h, 16))
+        return MOE_ERR_INVALID_ARG;
+    if ((st = check_ws(ws)) != MOE_OK) return st;
+    int sms = 0;
+    if ((st = device_info(&sms)) != MOE_OK) return st;
+    const WsLayout L = layout_of(s);
+    cudaError_t e = launch_grouped_gemm_train(3, *s, dy, nullptr, w_down, w_down, dg, du, h, g_q, u_q, scale, L, ws,
+                                              g_timeout_ns.load(), sms, (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_grouped_down_backward");
+}
+
+moe_status moe_grouped_swiglu_backward(const moe_shape *s, const void *dg, const void *du, const void *w_gate,
+                                       const void *w_up, void *dx_perm, void *ws, void *stream) {
+    moe_status st = check_shape(s);
+    if (st != MOE_OK) return st;
+    if (!aligned(dg, 16) || !aligned(du, 16) || !aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(dx_perm, 16))
+        return MOE_ERR_INVALID_ARG;
+    if ((st = check_ws(ws)) != MOE_OK) return st;
+    int sms = 0;
+    if ((st = device_info(&sms)) != MOE_OK) return st;
+    const WsLayout L = layout_of(s);
+    cudaError_t e = launch_grouped_gemm_train(4, *s, dg, du, w_gate, w_up, dx_perm, nullptr, nullptr, nullptr, nullptr,
+                                              nullptr, L, ws, g_timeout_ns.load(), sms, (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_grouped_swiglu_backward");
+}
+
+moe_status moe_gather_backward(const moe_shape *s, const void *dx_perm, const int32_t *dest_row, void *dx,
+                               void *stream) {
+    moe_status st = check_shape(s);
+    if (st != MOE_OK) return st;
+    if (!aligned(dx_perm, 16) || !aligned(dest_row, 4) || !aligned(dx, 16)) return MOE_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = device_info(&sms)) != MOE_OK) return st;
+    cudaError_t e = launch_gather_backward(*s, dx_perm, dest_row, dx, (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_gather_backward");
+}
+
+moe_status moe_grouped_swiglu_wgrad(const moe_shape *s, const void *x_perm, const void *dg, const void *du,
+                                    void *dw_gate, void *dw_up, void *ws, void *stream) {
+    moe_status st = check_shape(s);
+    if (st != MOE_OK) return st;
+    if (!aligned(x_perm, 16) || !aligned(dg, 16) || !aligned(du, 16) || !aligned(dw_gate, 16) || !aligned(dw_up, 16))
+        return MOE_ERR_INVALID_ARG;
+    if ((st = check_ws(ws)) != MOE_OK) return st;
+    int sms = 0;
+    if ((st = device_info(&sms)) != MOE_OK) return st;
+    const WsLayout L = layout_of(s);
+    cudaError_t e = launch_wgrad(*s, s->H, s->F, x_perm, dg, du, dw_gate, dw_up, L, ws, g_timeout_ns.load(), sms,
+                                 (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_grouped_swiglu_wgrad");
+}
+
+moe_status moe_grouped_down_wgrad(const moe_shape *s, const void *h, const void *dy, void *dw_down, void *ws,
+                                  void *stream) {
+    moe_status st = check_shape(s);
+    if (st != MOE_OK) return st;
+    if (!aligned(h, 16) || !aligned(dy, 16) || !aligned(dw_down, 16)) return MOE_ERR_INVALID_ARG;
+    if ((st = check_ws(ws)) != MOE_OK) return st;
+    int sms = 0;
+    if ((st = device_info(&sms)) != MOE_OK) return st;
+    const WsLayout L = layout_of(s);
+    cudaError_t e = launch_wgrad(*s, s->F, s->H, h, dy, nullptr, dw_down, nullptr, L, ws, g_timeout_ns.load(), sms,
+                                 (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_grouped_down_wgrad");
+}
+
+moe_status moe_backward(const moe_shape *s, const moe_backward_args *a, void *ws, void *stream) {
+    moe_status st = check_shape(s);
+    if (st != MOE_OK) return st;
+    // everything the steps would refuse is refused before the first of them is
+    // enqueued
+    if (!a || !aligned(a->dout, 16) || !aligned(a->y, 16) || !aligned(a->w_down, 16) || !aligned(a->g_q, 16) ||
+        !aligned(a->u_q, 16) || !aligned(a->scale, 2) || !aligned(a->topk_w, 4) || !aligned(a->dest_row, 4) ||
+        !aligned(a->dy, 16) || !aligned(a->dg, 16) || !aligned(a->du, 16) || !aligned(a->h, 16) ||
+        !aligned(a->dtopk_w, 4))
+        return MOE_ERR_INVALID_ARG;
+    if ((a->dlogits || a->rebuild_dispatch) && !aligned(a->topk_idx, 4)) return MOE_ERR_INVALID_ARG;
+    if (a->dlogits && !aligned(a->dlogits, 4)) return MOE_ERR_INVALID_ARG;
+    if (a->rebuild_dispatch &&
+        (!aligned(a->expert_counts, 4) || !aligned(a->expert_offsets, 4) || !aligned(a->src_token, 4)))
+        return MOE_ERR_INVALID_ARG;
+    const bool gate_up = a->dw_gate || a->dw_up;
+    if (gate_up && (!aligned(a->dw_gate, 16) || !aligned(a->dw_up, 16) || !aligned(a->x_perm, 16)))
+        return MOE_ERR_INVALID_ARG;
+    if (a->dw_down && !aligned(a->dw_down, 16)) return MOE_ERR_INVALID_ARG;
+    if (a->dx && (!aligned(a->dx, 16) || !aligned(a->dx_perm, 16) || !aligned(a->w_gate, 16) || !aligned(a->w_up, 16)))
+        return MOE_ERR_INVALID_ARG;
+    if ((st = check_ws(ws)) != MOE_OK) return st;
+    if (a->rebuild_dispatch &&
+        (st = moe_dispatch(s, a->topk_idx, a->expert_counts, a->expert_offsets, a->src_token, a->dest_row, ws,
+                           stream)) != MOE_OK)
+        return st;
+    st = moe_combine_backward(s, a->dout, a->y, a->dest_row, a->topk_w, a->topk_idx, a->dy, a->dtopk_w, a->dlogits,
+                              stream);
+    if (st != MOE_OK) return st;
+    st = moe_grouped_down_backward(s, a->dy, a->w_down, a->g_q, a->u_q, a->scale, a->dg, a->du, a->h, ws, stream);
+    if (st != MOE_OK) return st;
+    if (a->dw_down && (st = moe_grouped_down_wgrad(s, a->h, a->dy, a->dw_down, ws, stream)) != MOE_OK) return st;
+    if (gate_up &&
+        (st = moe_grouped_swiglu_wgrad(s, a->x_perm, a->dg, a->du, a->dw_gate, a->dw_up, ws, stream)) != MOE_OK)
+        return st;
+    if (!a->dx) return MOE_OK;
+    if ((st = moe_grouped_swiglu_backward(s, a->dg, a->du, a->w_gate, a->w_up, a->dx_perm, ws, stream)) != MOE_OK)
+        return st;
+    return moe_gather_backward(s, a->dx_perm, a->dest_row, a->dx, stream);
 }
 
 moe_status moe_quantize_weights_fp8(const moe_shape *s, int which, const void *w, void *w_q, float *w_scale,

@@ -643,6 +643,125 @@ MOE_API moe_status moe_ep_direct_down_return_fp8(const moe_shape *shape, int32_t
 MOE_API moe_status moe_ep_direct_quantize_h(const moe_shape *shape, int32_t G, const void *h_loc, void *h_q,
                                             float *h_scale, void *ep_ws, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Training: the layer's gradient, from an 8-bit activation checkpoint.  (The
+ * source pages stop at the forward path; these entry points are its chain
+ * rule.)  The forward pass is moe_forward_checkpoint: moe_forward whose SwiGLU
+ * GEMM also keeps the gate and up values g = x.Wg, u = x.Wu that the gradient
+ * needs, in 8 bits; the backward pass is moe_backward.  The conventions above
+ * hold for both and for the single steps below; like the forward GEMMs, the
+ * grouped ones read the schedule that the layer's dispatch left in `ws`.  When
+ * `ws` served another batch or layer in between, moe_dispatch rebuilds it from
+ * topk_idx (moe_backward does with args->rebuild_dispatch).
+ *
+ * Checkpoint format: OCP E4M3 codes of g and u, [P,F] each, with one scale per
+ * row and block of 32 features: scale[r][f/32][0] for g, [1] for u, a byte b
+ * standing for 2^(b-127), b = max(c + 119, 1) for the smallest integer c with
+ * max|v| <= 2^c over the block's finite values (1 for a block of zeros).  code
+ * = the nearest e4m3 value of v / 2^(b-127), ties to even (relative error at
+ * most 2^-4 down to 2^-13 of the block's largest value, absolute below); NaN
+ * and infinite values are stored as NaN.  Inside a block of 32, byte
+ * 4*(f%8) + f%32/8 is the code of feature f (the order in which the kernels
+ * hold them).  Rows not filled are left unwritten, as in h and y.
+ * ------------------------------------------------------------------------ */
+
+/* The index part of moe_permute (steps 2-3 without the row copy): counts,
+ * offsets, src_token, dest_row and the schedule in `ws`, from topk_idx. */
+MOE_API moe_status moe_dispatch(const moe_shape *shape, const int32_t *topk_idx, int32_t *expert_counts,
+                                int32_t *expert_offsets, int32_t *src_token, int32_t *dest_row, void *ws, void *stream);
+
+/* moe_grouped_swiglu (h is the same, bit for bit), writing the checkpoint too:
+ * g_q, u_q [P,F] codes (16-byte aligned), scale [P,F/32,2] bytes (2-byte
+ * aligned). */
+MOE_API moe_status moe_grouped_swiglu_checkpoint(const moe_shape *shape, const void *x_perm, const void *w_gate,
+                                                 const void *w_up, void *h, void *g_q, void *u_q, void *scale,
+                                                 void *ws, void *stream);
+
+/* moe_forward with moe_grouped_swiglu_checkpoint in place of
+ * moe_grouped_swiglu; args->x_perm must be given (the weights' gradient reads
+ * it), every output is moe_forward's. */
+MOE_API moe_status moe_forward_checkpoint(const moe_shape *shape, const moe_forward_args *args, void *g_q, void *u_q,
+                                          void *scale, void *ws, void *stream);
+
+/* Gradient of step 5.  dout [T,H] bf16 is the gradient of `out`; y, dest_row,
+ * topk_w as the forward pass left them.
+ *   dy[r]         = bf16( topk_w[t,j] * dout[t] ), r = dest_row[t*k+j]
+ *   dtopk_w[t,j]  = dout[t] . y[r]                              (fp32 sums)
+ *   dlogits[t,e]  = topk_w[t,j] (dtopk_w[t,j] - sum_i topk_w[t,i] dtopk_w[t,i])
+ *                   for e = topk_idx[t,j], 0 for every other e: the gradient
+ *                   through the softmax over the selected logits ([T,E] fp32,
+ *                   or NULL: not written, topk_idx unused).
+ * A token's experts are distinct (moe_route's are).  A row of dy that no pair
+ * maps to is left unwritten. */
+MOE_API moe_status moe_combine_backward(const moe_shape *shape, const void *dout, const void *y,
+                                        const int32_t *dest_row, const float *topk_w, const int32_t *topk_idx,
+                                        void *dy, float *dtopk_w, float *dlogits, void *stream);
+
+/* Gradient of step 4b and of the SwiGLU product.  dy [P,H] bf16; g, u from the
+ * checkpoint, s = 1 / (1 + exp(-g)):
+ *   dh = dy[r] . w_down[e][f,:]   (fp32, never written)
+ *   dg = bf16( dh u s (1 + g (1 - s)) ),  du = bf16( dh g s ),
+ *   h  = bf16( g s u ): the activations again, for moe_grouped_down_wgrad.
+ * dg, du, h [P,F]; rows not filled are left unwritten. */
+MOE_API moe_status moe_grouped_down_backward(const moe_shape *shape, const void *dy, const void *w_down,
+                                             const void *g_q, const void *u_q, const void *scale, void *dg, void *du,
+                                             void *h, void *ws, void *stream);
+
+/* Gradient of the gate and up projections with respect to their input:
+ *   dx_perm[r,c] = bf16( dg[r] . w_gate[e][c,:] + du[r] . w_up[e][c,:] ). */
+MOE_API moe_status moe_grouped_swiglu_backward(const moe_shape *shape, const void *dg, const void *du,
+                                               const void *w_gate, const void *w_up, void *dx_perm, void *ws,
+                                               void *stream);
+
+/* Gradient of the row copy: dx[t] = bf16( sum_j dx_perm[dest_row[t*k+j]] ),
+ * fp32 sums in slot order. */
+MOE_API moe_status moe_gather_backward(const moe_shape *shape, const void *dx_perm, const int32_t *dest_row, void *dx,
+                                       void *stream);
+
+/* Gradients of the expert weights, over the rows r of each expert (zeros for
+ * an expert without rows), fp32 sums rounded once to bf16:
+ *   dw_gate[e][c,f] = sum_r x_perm[r,c] dg[r,f],  dw_up likewise with du;
+ *   dw_down[e][f,c] = sum_r h[r,f] dy[r,c]. */
+MOE_API moe_status moe_grouped_swiglu_wgrad(const moe_shape *shape, const void *x_perm, const void *dg,
+                                            const void *du, void *dw_gate, void *dw_up, void *ws, void *stream);
+MOE_API moe_status moe_grouped_down_wgrad(const moe_shape *shape, const void *h, const void *dy, void *dw_down,
+                                          void *ws, void *stream);
+
+/* Every pointer argument of the layer's backward pass, for moe_backward. */
+typedef struct {
+    const void *dout;    /* [T,H] bf16 gradient of out */
+    const void *x_perm;  /* [P,H] as the forward pass left it (or moe_gather again) */
+    const void *y;       /* [P,H] as the forward pass left it */
+    const void *w_gate, *w_up, *w_down;    /* as in moe_forward_args */
+    const void *g_q, *u_q, *scale;         /* the checkpoint */
+    const int32_t *topk_idx;               /* [T,k] */
+    const float *topk_w;                   /* [T,k] */
+    int32_t *dest_row;                     /* [T*k] as the forward pass left it */
+    /* rebuild_dispatch != 0: the schedule in `ws` is not this batch's any
+     * more; it is rebuilt from topk_idx first, which writes dest_row (the same
+     * values) and the three below.  Otherwise they are unused and may be NULL. */
+    int32_t rebuild_dispatch;
+    int32_t *expert_counts, *expert_offsets, *src_token;
+    /* intermediates; dx_perm may be the same buffer as dy */
+    void *dy;                /* [P,H] */
+    void *dg, *du, *h;       /* [P,F] */
+    void *dx_perm;           /* [P,H] (unused with dx == NULL) */
+    /* results */
+    void *dx;                /* [T,H] bf16, or NULL: not wanted */
+    float *dtopk_w;          /* [T,k] */
+    float *dlogits;          /* [T,E], or NULL: not wanted */
+    void *dw_gate, *dw_up;   /* [E,H,F] bf16, or both NULL: not wanted */
+    void *dw_down;           /* [E,F,H] bf16, or NULL: not wanted */
+} moe_backward_args;
+
+/* The layer's backward pass on one stream: (moe_dispatch),
+ * moe_combine_backward, moe_grouped_down_backward, moe_grouped_down_wgrad,
+ * moe_grouped_swiglu_wgrad, moe_grouped_swiglu_backward, moe_gather_backward;
+ * the steps whose results are not wanted are left out.  The router's own
+ * weights get their gradient from dlogits: dW_r = x^T dlogits, dbias = its
+ * column sums, and dx gains dlogits W_r^T; those products are the caller's. */
+MOE_API moe_status moe_backward(const moe_shape *shape, const moe_backward_args *args, void *ws, void *stream);
+
 /* Upper bound, in nanoseconds, of every bounded device wait (default 1e9). */
 MOE_API void moe_set_wait_timeout_ns(uint64_t ns);
 
