@@ -11,7 +11,11 @@
 //   (two 128-row accumulators of 256 columns, all of tensor memory) of one
 //   expert, and its K loop walks the expert's row segments (uncapped: one;
 //   capacity layout: the capacity slots, then the overflow rows) in blocks of
-//   64 rows.  Units go to the CTAs in descending row count of their experts.
+//   64 rows.  Units are in descending row count of their experts and are dealt
+//   back and forth (CTA c takes unit c, 2n - 1 - c, 2n + c, ...): dealt in one
+//   direction, the first CTA gets the largest unit of every round, and under
+//   skew (8192 tokens, 128 experts, alpha 1) SMs idled 14% of the time: 416 ->
+//   380 us for gate and up, the same bits.
 // - Both operands are row-major [rows, features] and reduced over rows, so
 //   both are MN-major for the MMA and are loaded as they lie (64-feature x
 //   64-row boxes, 128-byte swizzle).
@@ -69,6 +73,12 @@ struct WUnit {
     int s0, l0, s1, l1;         // row segments
     int nkb;
 };
+
+// The CTA's unit of the next round.
+__device__ __forceinline__ int w_next(int &round) {
+    ++round;
+    return round * (int)gridDim.x + (int)(round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
 
 __device__ __forceinline__ bool w_decode(int u, const WgradArgs &a, WUnit &U) {
     const int per = a.m_tiles * a.n_tiles;
@@ -180,7 +190,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
             int issued_ph[kWStages];
             for (int s = 0; s < kWStages; ++s) issued_ph[s] = -1;
             bool ok = true;
-            for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+            for (int u = blockIdx.x, i = 0; u < total && ok; u = w_next(i)) {
                 WUnit U;
                 if (!w_decode(u, a, U)) {
                     atomicOr(a.status, MOE_DEV_BAD_ROW);
@@ -225,7 +235,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         uint32_t ph = 0, uses = 0;
         bool ok = true;
         const uint32_t base = smem_u32(smem);
-        for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+        for (int u = blockIdx.x, i = 0; u < total && ok; u = w_next(i)) {
             WUnit U;
             if (!w_decode(u, a, U)) continue;
             if (U.nkb == 0) continue;  // the epilogue writes zeros on its own
@@ -290,7 +300,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const uint32_t stg = smem_u32(staging + (warp - kWEpiWarp0) * kWStaging);
         const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + 128u * sub;
         uint32_t uses = 0;
-        for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        for (int u = blockIdx.x, i = 0; u < total; u = w_next(i)) {
             WUnit U;
             if (!w_decode(u, a, U)) continue;
             const bool mine = sub < U.nacc;
