@@ -46,7 +46,7 @@ cudaError_t launch_wgrad(const moe_shape &s, int MA, int NB, const void *A, cons
                          cudaStream_t stream);
 cudaError_t launch_combine_backward(const moe_shape &s, const void *dout, const void *y, const int32_t *dest_row,
                                     const float *topk_w, const int32_t *topk_idx, void *dy, float *dtopk_w,
-                                    float *dlogits, cudaStream_t stream);
+                                    float *dlogits, int num_sms, cudaStream_t stream);
 cudaError_t launch_gather_backward(const moe_shape &s, const void *dx_perm, const int32_t *dest_row, void *dx,
                                    cudaStream_t stream);
 int64_t ep_overflow_rows(const moe_shape &s, int G);
@@ -453,7 +453,7 @@ moe_status moe_combine_backward(const moe_shape *s, const void *dout, const void
         return MOE_ERR_INVALID_ARG;
     int sms = 0;
     if ((st = device_info(&sms)) != MOE_OK) return st;
-    cudaError_t e = launch_combine_backward(*s, dout, y, dest_row, topk_w, topk_idx, dy, dtopk_w, dlogits,
+    cudaError_t e = launch_combine_backward(*s, dout, y, dest_row, topk_w, topk_idx, dy, dtopk_w, dlogits, sms,
                                             (cudaStream_t)stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_combine_backward");
 }
