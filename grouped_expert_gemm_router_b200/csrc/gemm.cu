@@ -391,10 +391,8 @@ __device__ __forceinline__ void scale_frag(uint32_t (&r)[16], const float (&fs)[
 // word and neither the store here nor the load of mode 3 needs a transpose
 // (eight lanes x 4 bytes: one full 32-byte sector per row).
 
-// v, or NaN for an infinity (max(|.|) below then skips it, the code is NaN).
-__device__ __forceinline__ float nan_unless_finite(float v) { return v + (v - v); }
-
-// The exponent field of the smallest power of two >= |v| (0 for 0).
+// The exponent field of the smallest power of two >= |v| (0 for 0; 255 above
+// 2^127 and for an infinity).
 __device__ __forceinline__ uint32_t ceil_pow2_exp(float mag) { return (__float_as_uint(mag) + 0x7FFFFFu) >> 23; }
 
 // Scale byte of a block from its largest magnitude's exponent field.
@@ -402,44 +400,64 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t ex) { return ex > 9u ? e
 
 __device__ __forceinline__ int frag_reg(int fi, int ri) { return 8 * (fi >> 1) + 4 * (ri >> 1) + 2 * (fi & 1) + (ri & 1); }
 
+// Largest exponent field of each half of v over the eight lanes that hold one row.
+__device__ __forceinline__ uint32_t row_max_exp(uint32_t v) {
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) v = __vmaxu2(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
+           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3) << 16;
+}
+
 __device__ __forceinline__ void store_checkpoint(const GemmArgs &a, const Unit &U, int c0, int fbase, int lane,
-                                                 const uint32_t (&rg)[16], const uint32_t (&ru)[16]) {
+                                                 uint32_t (&rg)[16], uint32_t (&ru)[16]) {
     uint32_t ex[4];  // per row: exponent fields of gate (low half) and up (high half)
+#pragma unroll 1
+    for (;;) {
+        uint32_t most = 0u;
 #pragma unroll
-    for (int ri = 0; ri < 4; ++ri) {
-        float mg = 0.0f, mu = 0.0f;
+        for (int ri = 0; ri < 4; ++ri) {
+            float mg = 0.0f, mu = 0.0f;  // fmaxf passes over a NaN; its code comes out as NaN below
 #pragma unroll
-        for (int fi = 0; fi < 4; ++fi) {
-            mg = fmaxf(mg, fabsf(nan_unless_finite(__uint_as_float(rg[frag_reg(fi, ri)]))));
-            mu = fmaxf(mu, fabsf(nan_unless_finite(__uint_as_float(ru[frag_reg(fi, ri)]))));
+            for (int fi = 0; fi < 4; ++fi) {
+                mg = fmaxf(mg, fabsf(__uint_as_float(rg[frag_reg(fi, ri)])));
+                mu = fmaxf(mu, fabsf(__uint_as_float(ru[frag_reg(fi, ri)])));
+            }
+            ex[ri] = ceil_pow2_exp(mg) | (ceil_pow2_exp(mu) << 16);
+            most = max(most, max(__float_as_uint(mg), __float_as_uint(mu)));
         }
-        ex[ri] = ceil_pow2_exp(mg) | (ceil_pow2_exp(mu) << 16);
+        // Rare: an infinity in the warp's block becomes NaN, and the maxima
+        // are taken again without it.
+        if (!__any_sync(0xffffffffu, most == 0x7F800000u)) break;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float g = __uint_as_float(rg[j]), u = __uint_as_float(ru[j]);
+            rg[j] = __float_as_uint(g + (g - g));
+            ru[j] = __float_as_uint(u + (u - u));
+        }
     }
 #pragma unroll
     for (int ri = 0; ri < 4; ++ri) {
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) ex[ri] = __vmaxu2(ex[ri], __shfl_xor_sync(0xffffffffu, ex[ri], off));
-        const uint32_t bg = scale_byte(ex[ri] & 0xFFFFu), bu = scale_byte(ex[ri] >> 16);
+        const uint32_t e = row_max_exp(ex[ri]);
+        const uint32_t bg = scale_byte(e & 0xFFFFu), bu = scale_byte(e >> 16);
         // 1 / s = 2^(127 - b), a normal number for every b in [1, 247]
         const float ig = __uint_as_float((254u - bg) << 23), iu = __uint_as_float((254u - bu) << 23);
         const int row = unit_row(U, c0 + frag_row_offset(ri, lane));
         if (row < 0) continue;
-        float vg[4], vu[4];
+        float g[4], u[4];
 #pragma unroll
         for (int fi = 0; fi < 4; ++fi) {
-            vg[fi] = nan_unless_finite(__uint_as_float(rg[frag_reg(fi, ri)])) * ig;
-            vu[fi] = nan_unless_finite(__uint_as_float(ru[frag_reg(fi, ri)])) * iu;
+            g[fi] = __uint_as_float(rg[frag_reg(fi, ri)]) * ig;
+            u[fi] = __uint_as_float(ru[frag_reg(fi, ri)]) * iu;
         }
-        const size_t at = (size_t)row * a.n_out + fbase + 4 * (lane >> 2);
-        *reinterpret_cast<uint32_t *>(a.g_q + at) =
-            (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(vg[0], vg[1]), __NV_SATFINITE, __NV_E4M3) |
-            (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(vg[2], vg[3]), __NV_SATFINITE, __NV_E4M3) << 16;
-        *reinterpret_cast<uint32_t *>(a.u_q + at) =
-            (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(vu[0], vu[1]), __NV_SATFINITE, __NV_E4M3) |
-            (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(vu[2], vu[3]), __NV_SATFINITE, __NV_E4M3) << 16;
+        const size_t at = (size_t)row * a.n_out + fbase;
+        *reinterpret_cast<uint32_t *>(a.g_q + at + 4 * (lane >> 2)) = codes4(g[0], g[1], g[2], g[3]);
+        *reinterpret_cast<uint32_t *>(a.u_q + at + 4 * (lane >> 2)) = codes4(u[0], u[1], u[2], u[3]);
         if ((lane >> 2) == ri)  // one lane group per row writes its two scale bytes
-            *reinterpret_cast<uint16_t *>(a.ck_scale + ((size_t)row * (a.n_out / 32) + fbase / 32) * 2) =
-                (uint16_t)(bg | bu << 8);
+            *reinterpret_cast<uint16_t *>(a.ck_scale + at / 16) = (uint16_t)(bg | bu << 8);
     }
 }
 
@@ -1238,7 +1256,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         scale_frag(r0, fs0, rs);
                         if (U.nacc == 2) scale_frag(r1, fs1, rs);
                     }
-                    if (CKPT) store_checkpoint(a, U, c0, U.fx + q * 32, lane, r0, r1);
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
                         if (MODE == 0) {
@@ -1257,6 +1274,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
+                    // last: it may turn infinities into NaN
+                    if (CKPT) store_checkpoint(a, U, c0, U.fx + q * 32, lane, r0, r1);
                 }
             }
             // Hand the accumulator back to the MMA warp before the stores.
