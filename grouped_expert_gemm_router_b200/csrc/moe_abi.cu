@@ -428,7 +428,8 @@ moe_status moe_forward_checkpoint(const moe_shape *s, const moe_forward_args *a,
     // what the steps would refuse is refused before the first of them is enqueued
     if (!a || !aligned(a->x_perm, 16) || !aligned(g_q, 16) || !aligned(u_q, 16) || !aligned(scale, 2) ||
         !aligned(a->w_gate, 16) || !aligned(a->w_up, 16) || !aligned(a->w_down, 16) || !aligned(a->h, 16) ||
-        !aligned(a->y, 16) || !aligned(a->out, 16))
+        !aligned(a->y, 16) || !aligned(a->out, 16) || !aligned(a->x, 16) || !aligned(a->expert_counts, 4) ||
+        !aligned(a->expert_offsets, 4) || !aligned(a->src_token, 4) || !aligned(a->dest_row, 4))
         return MOE_ERR_INVALID_ARG;
     moe_status st = moe_route_dispatch(s, a->x, a->w_router, a->bias, a->logits, a->topk_idx, a->topk_w,
                                        a->expert_counts, a->expert_offsets, a->src_token, a->dest_row, ws, stream);

@@ -100,8 +100,10 @@ def test_forward_checkpoint_refuses_before_the_first_step(lib):
             setattr(a, n, v)
         return lib.moe_forward_checkpoint(ctypes.byref(s), ctypes.byref(a), *ck, PTR, None)
 
-    for n in ("x_perm", "w_gate", "w_up", "w_down", "h", "y", "out"):
+    for n in ("x", "x_perm", "w_gate", "w_up", "w_down", "h", "y", "out"):
         assert call(**{n: None}) == INVALID and call(**{n: PTR + 8}) == INVALID, n
+    for n in ("topk_idx", "topk_w", "expert_counts", "expert_offsets", "src_token", "dest_row"):
+        assert call(**{n: None}) == INVALID and call(**{n: PTR + 2}) == INVALID, n
     for i in range(3):
         ck = [PTR] * 3
         ck[i] = None

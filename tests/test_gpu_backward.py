@@ -41,7 +41,12 @@ CASES = {
     "capacity_unused": (50, 128, 256, 4, 2, 64, "uniform"),
     "capacity_zero": (90, 128, 128, 4, 2, 0, "skew"),
     "experts_256_k9": (96, 128, 128, 256, 9, None, "uniform"),
+    "experts_256_k256": (5, 128, 128, 256, 256, None, "uniform"),
     "long_rows": (4, 4096, 128, 3, 3, None, "uniform"),
+    # enough tokens for one warp each, and for four; an odd last block
+    "many_tokens": (4001, 384, 128, 4, 2, None, "uniform"),
+    "many_tokens_H1152": (901, 1152, 128, 8, 4, None, "skew"),
+    "capacity_long": (1500, 128, 256, 3, 2, 700, "skew"),
 }
 
 
