@@ -660,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(!COMBINE || MODE == 1, "the combine follows the down projection");
     static_assert(!FP8 || MODE < 2, "only the expert GEMMs of the forward pass run on fp8 operands");
     static_assert(!CKPT || (MODE == 0 && !FP8), "the checkpoint is taken from the bf16 SwiGLU GEMM");
+    constexpr bool kWarpIssue = MODE >= 3 || CKPT;  // the MMA warp stays together (tc_mma_bf16_warp)
     constexpr bool kKMajorA = MODE >= 3;      // bf16 weights with the reduction dimension contiguous
     constexpr bool kDown = MODE == 1 || MODE == 4;  // plain bf16 results, 128- or 256-feature units
     constexpr int kStageK = FP8 ? 128 : kBK;  // K elements per stage: 128 bytes of each row
@@ -962,7 +963,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------- MMA issuer ----
-        if (lane == 0) {
+        if (kWarpIssue || lane == 0) {
+            // a wait's outcome, the same for the whole warp where it issues together
+            auto waited = [&](uint64_t *bar, uint32_t parity) -> bool {
+                const bool w = mbar_wait_bounded(bar, parity, a.timeout_ns, s_abort);
+                return kWarpIssue ? (bool)__all_sync(0xffffffffu, w) : w;
+            };
+            auto mma = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t acc) {
+                if (kWarpIssue) tc_mma_bf16_warp(d, ad, bd, id, acc);
+                else tc_mma_bf16(d, ad, bd, id, acc);
+            };
+            auto commit = [&](uint64_t *bar) {
+                if (kWarpIssue) tc_commit_warp(bar);
+                else tc_commit(bar);
+            };
             int sa = 0, sb = 0;
             uint32_t pha = 0, phb = 0;
             TmemPlan plan;
@@ -978,15 +992,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 plan.place(tmem_width<MODE>(U), h, big);  // mode 2 uses all of tensor memory
                 const uint32_t d0 = tmem + h * 256u, d1 = big ? tmem + 256u : d0 + 128u;
                 // wait until the epilogue has drained the half(s) this unit takes
-                ok = mbar_wait_bounded(&tempty[h], (plan.uses[h] & 1u) ^ 1u, a.timeout_ns, s_abort);
-                if (ok && big) ok = mbar_wait_bounded(&tempty[1], (plan.uses[1] & 1u) ^ 1u, a.timeout_ns, s_abort);
+                ok = waited(&tempty[h], (plan.uses[h] & 1u) ^ 1u);
+                if (ok && big) ok = waited(&tempty[1], (plan.uses[1] & 1u) ^ 1u);
                 if (!ok) break;
                 tc_fence_after();
                 const int kb0 = MODE == 2 ? U.fb * a.route_kb : 0;
                 const int kb1 = MODE == 2 ? min(nk, kb0 + a.route_kb) : nk;
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait_bounded(&fullA[sa], pha, a.timeout_ns, s_abort) ||
-                        !mbar_wait_bounded(&fullB[sb], phb, a.timeout_ns, s_abort)) {
+                    if (!waited(&fullA[sa], pha) || !waited(&fullB[sb], phb)) {
                         ok = false;
                         break;
                     }
@@ -1025,16 +1038,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t a0desc =
                             kKMajorA ? sdesc_sw128(sa0 + kk * 32, 16, 1024) : sdesc_sw128(sa0 + kk * 2048, kABox, 1024);
                         const uint32_t accum = (kb | kk) ? 1u : 0u;
-                        tc_mma_bf16(d0, a0desc, bdesc, idesc, accum);
+                        mma(d0, a0desc, bdesc, idesc, accum);
                         if (U.nacc == 2) {
                             const uint64_t a1desc = kKMajorA ? sdesc_sw128(sa1 + kk * 32, 16, 1024)
                                                              : sdesc_sw128(sa1 + kk * 2048, kABox, 1024);
-                            tc_mma_bf16(d1, a1desc, bdesc, idesc, accum);
+                            mma(d1, a1desc, bdesc, idesc, accum);
                         }
                     }
                     // each stage is freed once these MMAs have read it
-                    tc_commit(&emptyA[sa]);
-                    tc_commit(&emptyB[sb]);
+                    commit(&emptyA[sa]);
+                    commit(&emptyB[sb]);
                     if (++sa == na) {
                         sa = 0;
                         pha ^= 1u;
@@ -1045,14 +1058,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!ok) break;
-                tc_commit(&tfull[h]);
-                if (big) tc_commit(&tfull[1]);
+                commit(&tfull[h]);
+                if (big) commit(&tfull[1]);
                 plan.advance(big, h);
             }
-            if (!ok && !*s_abort) raise_abort(s_abort, a.status);
+            if (!ok && lane == 0 && !*s_abort) raise_abort(s_abort, a.status);
             // All MMAs issued by this thread complete before tensor memory is freed.
             int never = 0;
-            tc_commit(mma_done);
+            commit(mma_done);
             mbar_wait_bounded(mma_done, 0, a.timeout_ns, &never);
         }
         __syncwarp();
