@@ -261,37 +261,34 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 }
                 __syncwarp();
                 tc_fence_after();
-                if (lane == 0) {
-                    const int steps = (n + 15) >> 4;
-                    for (int kk = 0; kk < steps; ++kk) {
-                        // both operands MN-major: 16 rows (2 KiB) per MMA, the 64-feature boxes 8 KiB apart
-                        const uint64_t bdesc = sdesc_sw128(sb + kk * 2048, kWBox, 1024);
-                        const uint32_t accum = (kb | kk) ? 1u : 0u;
-                        tc_mma_bf16(tmem, sdesc_sw128(sa + kk * 2048, kWBox, 1024), bdesc, idesc, accum);
-                        if (U.macc == 2)
-                            tc_mma_bf16(tmem + 256u, sdesc_sw128(sa + kWHalf + kk * 2048, kWBox, 1024), bdesc, idesc,
-                                        accum);
-                    }
-                    tc_commit(&empty[stage]);
+                const int steps = (n + 15) >> 4;
+#pragma unroll
+                for (int kk = 0; kk < kWBK / 16; ++kk) {
+                    if (kk >= steps) break;
+                    // both operands MN-major: 16 rows (2 KiB) per MMA, the 64-feature boxes 8 KiB apart
+                    const uint64_t bdesc = sdesc_sw128(sb + kk * 2048, kWBox, 1024);
+                    const uint32_t accum = (kb | kk) ? 1u : 0u;
+                    tc_mma_bf16_warp(tmem, sdesc_sw128(sa + kk * 2048, kWBox, 1024), bdesc, idesc, accum);
+                    if (U.macc == 2)
+                        tc_mma_bf16_warp(tmem + 256u, sdesc_sw128(sa + kWHalf + kk * 2048, kWBox, 1024), bdesc, idesc,
+                                         accum);
                 }
-                __syncwarp();
+                tc_commit_warp(&empty[stage]);
                 if (++stage == kWStages) {
                     stage = 0;
                     ph ^= 1u;
                 }
             }
             if (!ok) break;
-            if (lane == 0) tc_commit(tfull);
-            __syncwarp();
+            tc_commit_warp(tfull);
             ++uses;
         }
-        if (lane == 0) {
-            if (!ok && !*s_abort) w_abort(s_abort, a.status);
-            // All MMAs issued by this thread complete before tensor memory is freed.
-            int never = 0;
-            tc_commit(mma_done);
-            mbar_wait_bounded(mma_done, 0, a.timeout_ns, &never);
-        }
+        if (!ok && lane == 0 && !*s_abort) w_abort(s_abort, a.status);
+        __syncwarp();
+        // All MMAs issued by this warp complete before tensor memory is freed.
+        int never = 0;
+        tc_commit_warp(mma_done);
+        mbar_wait_bounded(mma_done, 0, a.timeout_ns, &never);
         __syncwarp();
     } else if (warp >= kWEpiWarp0) {
         // ---------------------------------------------------- epilogue ----
