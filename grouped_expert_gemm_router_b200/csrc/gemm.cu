@@ -107,6 +107,13 @@ constexpr int kEpiWarps = 16;                  // four per tensor-memory lane qu
 constexpr int kEpiSub = kEpiWarps / 4;         // warps sharing one lane quarter
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr uint32_t kTmemCols = 512;
+// Mode 3 (see its epilogue): 256-feature units from this reduction length up.
+// Their epilogue, the longest of all modes, is not overlapped, a fixed cost
+// per unit that the halved re-reading of the token rows pays back on long
+// reductions: K 4096 (4096 rows, 8 experts) 671 -> 628 us and K 3584 190 ->
+// 178 us, K 2560 457 -> 449 or 409 -> 424, K 2048 (65536 rows, 128 experts)
+// 328 -> 358 us back to back.
+constexpr int kWideMinK = 3584;
 
 struct GemmArgs {
     const int4 *tile_map;
@@ -249,7 +256,7 @@ __device__ __forceinline__ void decode_unit(int u, const int *gts, const GemmArg
     U.n0p = (U.p0l + 15) & ~15;
     U.N = U.n0p + ((U.p1l + 15) & ~15);
     U.fx = U.fb * fbw;
-    U.nacc = (MODE == 0) ? 2 : ((fbw == 256 && U.fx + 128 < a.n_out) ? 2 : 1);  // mode 3: fbw = 128
+    U.nacc = (MODE == 0) ? 2 : ((fbw == 256 && U.fx + 128 < a.n_out) ? 2 : 1);
     U.valid = (unsigned)U.e < (unsigned)a.E && U.N > 0 && U.N <= trows && U.p0s >= 0 && U.p1s >= 0 &&
               U.p0s + U.p0l <= a.P && U.p1s + U.p1l <= a.P && U.fb < num_fb;
 }
@@ -718,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     pdl_wait();  // the schedule and the token rows come from earlier kernels
     int total, trows;
-    int num_fb = a.num_fb, fbw = MODE == 0 || MODE == 3 ? 128 : 256;
+    int num_fb = a.num_fb, fbw = MODE == 0 ? 128 : 256;
     if (MODE == 2) {
         total = (a.T + a.route_rows - 1) / a.route_rows * a.route_q;
         trows = a.route_rows;
@@ -735,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int grid = (int)gridDim.x;
         const int tr = *a.tile_rows;
         const int r256 = (nt * a.num_fb + grid - 1) / grid, r128 = (nt * (a.n_out / 128) + grid - 1) / grid;
-        if (kDown && r128 * (128 + tr) < r256 * (256 + tr)) {
+        if ((kDown || MODE == 3) && (r128 * (128 + tr) < r256 * (256 + tr) || (MODE == 3 && a.K < kWideMinK))) {
             num_fb = a.n_out / 128;
             fbw = 128;
         }
@@ -1147,12 +1154,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             if (MODE == 3) {
-                // One accumulator of up to 256 columns in one half (its
-                // epilogue overlaps the next unit's MMAs): dh stays in fp32.
+                // dh stays in fp32 (its 256 KB are all of the register file, so
+                // it cannot wait there).  Units in one half of tensor memory
+                // overlap the next unit's MMAs; a unit in both halves hands
+                // back accumulator 0 while accumulator 1 is still read.
 #pragma unroll 1
-                for (int c0 = sub * 16; c0 < U.N; c0 += 16 * kEpiSub)
-                    swiglu_backward_chunk(a, U, t0, c0, U.fx + q * 32, lane, stg);
-                release();
+                for (int acc = 0; acc < U.nacc; ++acc) {
+#pragma unroll 1
+                    for (int c0 = sub * 16; c0 < U.N; c0 += 16 * kEpiSub)
+                        swiglu_backward_chunk(a, U, acc ? t1 : t0, c0, U.fx + 128 * acc + q * 32, lane, stg);
+                    if (acc == 0 && big) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&tempty[0]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty[big ? 1 : h]);
                 plan.advance(big, h);
                 continue;
             }
@@ -1531,7 +1550,7 @@ cudaError_t launch_grouped_gemm_train(int mode, const moe_shape &s, const void *
     a.ck_scale = (uint8_t *)ck_scale;
     a.n_out = n_out;
     a.K = mode == 4 ? 2 * s.F : s.H;
-    a.num_fb = mode == 4 ? (s.H + 255) / 256 : s.F / 128;
+    a.num_fb = mode == 0 ? s.F / 128 : (n_out + 255) / 256;
     a.E = s.E;
     a.P = (int)P;
     a.max_tiles = L.max_tiles;

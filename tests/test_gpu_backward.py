@@ -47,6 +47,9 @@ CASES = {
     "many_tokens": (4001, 384, 128, 4, 2, None, "uniform"),
     "many_tokens_H1152": (901, 1152, 128, 8, 4, None, "skew"),
     "capacity_long": (1500, 128, 256, 3, 2, 700, "skew"),
+    # long reductions: 256-feature units (here of full and of ragged row tiles, and an odd last feature block)
+    "wide_units": (700, 3584, 384, 2, 1, None, "uniform"),
+    "wide_units_capacity": (400, 3712, 640, 2, 1, 130, "uniform"),
 }
 
 
