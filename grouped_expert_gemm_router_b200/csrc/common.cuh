@@ -407,8 +407,10 @@ __device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t adesc, uin
 }
 // The same two for a warp that stays together: every lane calls, one elected
 // lane (always the same) issues.  The instructions take their operands from
-// the warp's uniform registers; a lane that is alone in a branch fills them at
-// a cost of about 70 cycles per MMA.
+// the warp's uniform registers, which a lane alone in a branch fills the
+// slower way: with the whole warp a K block's issue takes 50-60 cycles less
+// (546 -> 491 for four small MMAs, 863 -> 777 for eight large ones), the
+// kernels 4-11%.
 __device__ __forceinline__ void tc_commit_warp(uint64_t *bar) {
     asm volatile(
         "{\n\t.reg .pred q;\n\t"

@@ -16,7 +16,6 @@
 //           inside a unit the K blocks rotate over route_groups accumulators
 //           (block j of the range to accumulator j mod route_groups) and the
 //           epilogue adds them in fp32 in a fixed order.
-//
 //   mode 3, gradient of the down projection and of the SwiGLU product (no
 //           counterpart on the pages: the chain rule of modes 1 and 0):
 //           dh[r, f] = dy[r] . Wd[e][f, :], kept in fp32; with g, u from the
@@ -28,6 +27,17 @@
 //           those of the up half, into the same accumulator.
 //   Modes 3 and 4 reduce over the weights' contiguous dimension, so their
 //   weight operand is K-major where modes 0-2 have it MN-major.
+//   Few rows per expert: bound by the weights' bytes from HBM (T 128, 64
+//   experts, capacity layout: checkpoint GEMM 117 us, 6.4 TB/s).  Many rows: a
+//   unit's K block moves its operands through shared memory twice (TMA writes,
+//   MMA reads) at 128 bytes a cycle, 1109 cycles for 206 rows x 256 features
+//   against 820 of MMA, and the units together take what L2 delivers, 13 TB/s
+//   (65536 rows, 128 experts, H 2048, F 768: mode 3 267 us, checkpoint GEMM
+//   421 us; 4096 rows, 8 experts, H 4096, F 14336: mode 4 882 us, where three
+//   rounds of 107 CTAs leave a third of the SM time idle; handing units out
+//   from a counter, or in smaller pieces, evens that out and is slower: CTAs
+//   that run the row tiles of one expert side by side share its weights in L2).
+//   At the 1000 W cap, back to back, 325, 489 and 1065 us.
 //
 // Design (B200 first, not the page's Triton kernel):
 // - Swap-AB.  The MMA computes D[feature, row] = W^T[feature, k] * X^T[k, row]:
