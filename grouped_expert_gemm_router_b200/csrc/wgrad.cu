@@ -336,7 +336,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 for (int i = 0; i < 2 * U.macc; ++i) put(i >> 1, i & 1);
                 continue;
             }
-            const bool got = mbar_wait_bounded(tfull, uses & 1u, a.timeout_ns, s_abort);
+            // this wait lasts for the whole reduction (under 0.1 s per 65536 blocks)
+            const uint64_t limit = a.timeout_ns * (1u + (uint32_t)U.nkb / 65536u);
+            const bool got = mbar_wait_bounded(tfull, uses & 1u, limit, s_abort);
             if (!__all_sync(0xffffffffu, got)) {
                 if (lane == 0 && !*s_abort) w_abort(s_abort, a.status);
                 break;

@@ -406,7 +406,7 @@ def test_layer_gradient(name):
             assert abs(diff - float((ps[i].grad * v).sum())) <= 1e-5 * abs(diff) + 1e-6
 
 
-@pytest.mark.parametrize("name", ["two_tiles", "capacity", "empty_experts"])
+@pytest.mark.parametrize("name", ["two_tiles", "capacity", "empty_experts", "many_tokens", "wide_units"])
 def test_backward_is_its_steps_and_repeats(name):
     """moe_backward gives the single steps' results bit for bit, twice over;
     with dx, dlogits or weight gradients not wanted the others are the same;
@@ -443,6 +443,32 @@ def test_backward_is_its_steps_and_repeats(name):
     for n in RESULTS:
         assert torch.equal(d[n], ref[n]), n
     assert moe.moe_read_status(ws) == 0
+
+
+@pytest.mark.parametrize("name", ["two_tiles", "capacity", "many_tokens"])
+def test_forward_checkpoint_in_every_form_of_the_layer(name):
+    """The combine inside the down GEMM and logits given by the caller: out
+    and the gradients of the plain form, bit for bit."""
+    L = Layer(name)
+    wr = torch.randn(L.H, L.E, generator=L.gen, device="cuda") / L.H ** 0.5
+    dout = L.randn(L.T, L.H)
+    ref = _forward_backward(L, wr, dout)
+    s = L.shape
+    for flags in (moe.MOE_FLAG_FUSED_COMBINE, moe.MOE_FLAG_LOGITS_IN):
+        L.shape = moe.make_shape(s.T, s.H, s.F, s.E, s.k, C=s.C, flags=s.flags | flags)
+        b = moe.alloc_buffers(L.shape)
+        b["logits"].copy_(ref["logits"])
+        b.update(x=L.x, w_router=wr, bias=None, w_gate=L.w_gate, w_up=L.w_up, w_down=L.w_down)
+        b.update(moe.alloc_checkpoint(L.shape))
+        moe.moe_forward_checkpoint(L.shape, b, b["ws"])
+        out = b["out"].clone()
+        b.update(moe.alloc_backward_buffers(L.shape))
+        b["dout"] = dout
+        moe.moe_backward(L.shape, b, b["ws"])
+        assert torch.equal(out, ref["out"])
+        for n in RESULTS:
+            assert torch.equal(b[n], ref[n]), n
+        assert moe.moe_read_status(b["ws"]) == 0
 
 
 def test_backward_captured_and_replayed_on_new_inputs():
