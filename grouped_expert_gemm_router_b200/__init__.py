@@ -231,21 +231,29 @@ def make_shape(T, H, F, E, k, C=0, capacity=False, logits_in=False, flags=0) -> 
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    try:
+        return t.data_ptr()
+    except AttributeError:  # None, or an address
+        if t is None or isinstance(t, int):
+            return t
+        raise
+
+
+_raw_stream = None  # (current device, its current stream's handle), once CUDA is up
 
 
 def _stream(stream):
+    global _raw_stream
     if stream is None:
-        import torch
-        if torch.cuda.is_initialized():
-            # the handle alone: the Stream object of torch.cuda.current_stream
-            # costs 3 us, more than a small call's launch
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            import torch
+            s = torch.cuda.current_stream().cuda_stream  # initialises CUDA
+            _raw_stream = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+            return s
+        # the handle alone: the Stream object of torch.cuda.current_stream
+        # costs 3 us, more than a small call's launch
+        device, handle = _raw_stream
+        return handle(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
