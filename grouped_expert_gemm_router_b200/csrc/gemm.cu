@@ -32,12 +32,12 @@
 //   unit's K block moves its operands through shared memory twice (TMA writes,
 //   MMA reads) at 128 bytes a cycle, 1109 cycles for 206 rows x 256 features
 //   against 820 of MMA, and the units together take what L2 delivers, 13 TB/s
-//   (65536 rows, 128 experts, H 2048, F 768: mode 3 267 us, checkpoint GEMM
-//   421 us; 4096 rows, 8 experts, H 4096, F 14336: mode 4 882 us, where three
+//   (65536 rows, 128 experts, H 2048, F 768: mode 3 268 us, checkpoint GEMM
+//   409 us; 4096 rows, 8 experts, H 4096, F 14336: mode 4 844 us, where three
 //   rounds of 107 CTAs leave a third of the SM time idle; handing units out
 //   from a counter, or in smaller pieces, evens that out and is slower: CTAs
 //   that run the row tiles of one expert side by side share its weights in L2).
-//   At the 1000 W cap, back to back, 325, 489 and 1065 us.
+//   At the 1000 W cap, back to back, 323, 478 and 995 us.
 //
 // Design (B200 first, not the page's Triton kernel):
 // - Swap-AB.  The MMA computes D[feature, row] = W^T[feature, k] * X^T[k, row]:
@@ -124,6 +124,17 @@ constexpr uint32_t kTmemCols = 512;
 // 178 us, K 2560 457 -> 449 or 409 -> 424, K 2048 (65536 rows, 128 experts)
 // 328 -> 358 us back to back.
 constexpr int kWideMinK = 3584;
+// Training GEMMs: the row tiles of an expert (uncapped: one run of rows) are
+// made equally high, in 16s, instead of 256, 256, ..., rest as the schedule has
+// them: the same products and the same bits, but the CTAs that share the
+// expert's weights stay in step and the units of a round cost the same (mode 4,
+// 4096 rows, 8 experts: 1016 -> 985 us; mode 3 there 590 -> 570; checkpoint
+// GEMM, 65536 rows, 128 experts: 470 -> 465).  Not for 128-feature units of
+// mode 3, whose short rest tiles hide behind the epilogue (312 -> 326).  Up to
+// this many tiles, where rounding to 16 cannot use the last tile up: n > 256
+// (nt - 1) rows leave it more than n/nt - 16 (nt - 1) - 16 > 0; beyond, the rest
+// is a small share.
+constexpr int kEvenTiles = 8;
 
 struct GemmArgs {
     const int4 *tile_map;
@@ -173,6 +184,7 @@ struct GemmArgs {
     // by mode 3): e4m3 codes [P][n_out] of gate and up, and per (row, 32
     // features) one scale byte each, [P][n_out / 32][2]
     uint8_t *g_q, *u_q, *ck_scale;
+    int capped;  // capacity layout
     __nv_bfloat16 *out_du, *out_h;  // mode 3: du and h beside out = dg
 };
 
@@ -220,7 +232,7 @@ struct Unit {
     bool valid;  // false only for a corrupt schedule: every role then skips the unit
 };
 
-template <int MODE>
+template <int MODE, bool EVEN = false>
 // num_fb / fbw: feature blocks per row tile and their width (mode 0: 128
 // features, gate and up; mode 1: 256 features in two accumulators, or 128 in
 // one when that still fits one wave).
@@ -263,6 +275,13 @@ __device__ __forceinline__ void decode_unit(int u, const int *gts, const GemmArg
     U.p0l = d.z & 0xFFFF;
     U.p1l = (d.z >> 16) & 0xFFFF;
     U.p1s = d.w;
+    if (EVEN && (MODE != 3 || fbw == 256) && nt > 1 && nt <= kEvenTiles && !a.capped) {
+        const int4 first = a.tile_map[g0], last = a.tile_map[g0 + nt - 1];
+        const int n = last.y + (last.z & 0xFFFF) - first.y;
+        const int h = ((n + nt - 1) / nt + 15) & ~15;
+        U.p0s = first.y + (tile - g0) * h;
+        U.p0l = min(h, n - (tile - g0) * h);
+    }
     U.n0p = (U.p0l + 15) & ~15;
     U.N = U.n0p + ((U.p1l + 15) & ~15);
     U.fx = U.fb * fbw;
@@ -678,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(!FP8 || MODE < 2, "only the expert GEMMs of the forward pass run on fp8 operands");
     static_assert(!CKPT || (MODE == 0 && !FP8), "the checkpoint is taken from the bf16 SwiGLU GEMM");
     constexpr bool kWarpIssue = MODE >= 3 || CKPT;  // the MMA warp stays together (tc_mma_bf16_warp)
+    constexpr bool kEven = MODE >= 3 || CKPT;       // row tiles of an expert made equally high
     constexpr bool kKMajorA = MODE >= 3;      // bf16 weights with the reduction dimension contiguous
     constexpr bool kDown = MODE == 1 || MODE == 4;  // plain bf16 results, 128- or 256-feature units
     constexpr int kStageK = FP8 ? 128 : kBK;  // K elements per stage: 128 bytes of each row
@@ -817,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < kMaxBStages; ++s) issued_ph[s] = -1;
         for (int u = blockIdx.x; u < total; u += stride) {
             Unit U;
-            decode_unit<MODE>(u, s_gts, a, trows, num_fb, fbw, U);
+            decode_unit<MODE, kEven>(u, s_gts, a, trows, num_fb, fbw, U);
             if (!U.valid) continue;
             // The unit's tokens, one per tile row; padding rows repeat the
             // first row (their results are never stored).  Loads already
@@ -884,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < kMaxAStages; ++s) issued_ph[s] = -1;
             for (int u = blockIdx.x; u < total; u += stride) {
                 Unit U;
-                decode_unit<MODE>(u, s_gts, a, trows, num_fb, fbw, U);
+                decode_unit<MODE, kEven>(u, s_gts, a, trows, num_fb, fbw, U);
                 if (!U.valid) {
                     if (is_a) atomicOr(a.status, MOE_DEV_BAD_ROW);
                     continue;
@@ -1001,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int u = blockIdx.x; u < total && ok; u += stride) {
                 Unit U;
-                decode_unit<MODE>(u, s_gts, a, trows, num_fb, fbw, U);
+                decode_unit<MODE, kEven>(u, s_gts, a, trows, num_fb, fbw, U);
                 if (!U.valid) continue;
                 const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, U.N) : idesc_bf16_f32(128, U.N, kKMajorA ? 0 : 1, 0);
                 uint32_t h;
@@ -1096,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         TmemPlan plan;
         for (int u = blockIdx.x; u < total; u += stride) {
             Unit U;
-            decode_unit<MODE>(u, s_gts, a, trows, num_fb, fbw, U);
+            decode_unit<MODE, kEven>(u, s_gts, a, trows, num_fb, fbw, U);
             if (!U.valid) continue;
             // FP8: the scales of this thread's four features in each accumulator
             float fs0[4] = {1.0f, 1.0f, 1.0f, 1.0f}, fs1[4] = {1.0f, 1.0f, 1.0f, 1.0f};
@@ -1558,6 +1578,7 @@ cudaError_t launch_grouped_gemm_train(int mode, const moe_shape &s, const void *
     a.g_q = (uint8_t *)g_q;
     a.u_q = (uint8_t *)u_q;
     a.ck_scale = (uint8_t *)ck_scale;
+    a.capped = (s.flags & MOE_FLAG_CAPACITY) != 0;
     a.n_out = n_out;
     a.K = mode == 4 ? 2 * s.F : s.H;
     a.num_fb = mode == 0 ? s.F / 128 : (n_out + 255) / 256;
