@@ -50,6 +50,9 @@ CASES = {
     # long reductions: 256-feature units (here of full and of ragged row tiles, and an odd last feature block)
     "wide_units": (700, 3584, 384, 2, 1, None, "uniform"),
     "wide_units_capacity": (400, 3712, 640, 2, 1, 130, "uniform"),
+    "wide_unit_one_block": (300, 3584, 128, 1, 1, None, "uniform"),
+    # more row tiles than are made equally high
+    "eleven_tiles": (2600, 128, 256, 1, 1, None, "uniform"),
 }
 
 
