@@ -225,6 +225,23 @@ inline cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, 
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+
+// Lets a kernel be launched with `bytes` of dynamic shared memory (above the
+// default 48 KB) on the current device.  Called before every such launch: the
+// attribute belongs to the device that is current then, not to the process,
+// and several host threads may launch at once.
+template <typename... Params>
+inline cudaError_t allow_smem(void (*kernel)(Params...), size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+// launch_pdl of a kernel that needs allow_smem.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_pdl_smem(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                   Args... args) {
+    const cudaError_t e = allow_smem(kernel, smem);
+    return e == cudaSuccess ? launch_pdl(kernel, grid, block, smem, stream, args...) : e;
+}
 #endif
 
 // ------------------------------------------------------------ device helpers --

@@ -1441,14 +1441,8 @@ cudaError_t launch_router_logits_tc(const moe_shape &s, const void *x, const flo
     a.route_kb = plan.kb;
     a.route_groups = plan.groups;
     a.row_boxes = boxes;
-    static bool attr_done = false;
-    if (!attr_done) {
-        err = cudaFuncSetAttribute(k_grouped_gemm<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-        if (err != cudaSuccess) return err;
-        attr_done = true;
-    }
     *q = plan.q;
-    return launch_pdl(k_grouped_gemm<2>, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA, tA, tB, a);
+    return launch_pdl_smem(k_grouped_gemm<2>, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA, tA, tB, a);
 }
 
 // mode 0: act = x_perm [P,H], w0 = gate, w1 = up, out = h [P,F]
@@ -1496,8 +1490,11 @@ cudaError_t launch_grouped_gemm(int mode, const moe_shape &s, const void *act, c
     a.row_boxes = boxes;
     a.stall_first_stage = (mode == 0 && !gather && (s.flags & MOE_FLAG_TEST_STALL_GEMM)) ? 1 : 0;
     a.row_addr = (mode == 1 && !comb) ? row_addr : nullptr;
-    static bool attr_done[6] = {false, false, false, false, false, false};
-    cudaError_t err;
+    auto go = [&](auto kernel) {
+        const cudaError_t e =
+            launch_pdl_smem(kernel, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA0, tA1, tB, a);
+        return e == cudaSuccess ? cudaGetLastError() : e;
+    };
     if (mode == 1 && comb) {
         a.src_token = comb->src_token;
         a.dest_row = comb->dest_row;
@@ -1505,41 +1502,10 @@ cudaError_t launch_grouped_gemm(int mode, const moe_shape &s, const void *act, c
         a.comb_out = (__nv_bfloat16 *)comb->out;
         a.comb_cnt = (int *)((char *)ws + L.combine_cnt);
         a.k = s.k;
-        if (!attr_done[5]) {
-            err = cudaFuncSetAttribute(k_grouped_gemm<1, false, false, true>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-            if (err != cudaSuccess) return err;
-            attr_done[5] = true;
-        }
-        err = launch_pdl(k_grouped_gemm<1, false, false, true>, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA0, tA1, tB, a);
-        if (err != cudaSuccess) return err;
-    } else if (gather) {
-        if (!attr_done[2]) {
-            err = cudaFuncSetAttribute(k_grouped_gemm<0, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kSmemBytes);
-            if (err != cudaSuccess) return err;
-            attr_done[2] = true;
-        }
-        err = launch_pdl(k_grouped_gemm<0, true>, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA0, tA1, tB, a);
-        if (err != cudaSuccess) return err;
-    } else if (mode == 0) {
-        if (!attr_done[0]) {
-            err = cudaFuncSetAttribute(k_grouped_gemm<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-            if (err != cudaSuccess) return err;
-            attr_done[0] = true;
-        }
-        err = launch_pdl(k_grouped_gemm<0>, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA0, tA1, tB, a);
-        if (err != cudaSuccess) return err;
-    } else {
-        if (!attr_done[1]) {
-            err = cudaFuncSetAttribute(k_grouped_gemm<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-            if (err != cudaSuccess) return err;
-            attr_done[1] = true;
-        }
-        err = launch_pdl(k_grouped_gemm<1>, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA0, tA1, tB, a);
-        if (err != cudaSuccess) return err;
+        return go(k_grouped_gemm<1, false, false, true>);
     }
-    return cudaGetLastError();
+    if (gather) return go(k_grouped_gemm<0, true>);
+    return mode == 0 ? go(k_grouped_gemm<0>) : go(k_grouped_gemm<1>);
 }
 
 // mode 0 with the 8-bit checkpoint: as launch_grouped_gemm mode 0 on x_perm.
@@ -1588,11 +1554,8 @@ cudaError_t launch_grouped_gemm_train(int mode, const moe_shape &s, const void *
     a.timeout_ns = timeout_ns;
     a.T = s.T;
     a.row_boxes = boxes;
-    auto go = [&](auto kernel, const auto &tB_) -> cudaError_t {
-        // set on every call: the attribute belongs to the current device
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-        if (e != cudaSuccess) return e;
-        return launch_pdl(kernel, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA0, tA1, tB_, a);
+    auto go = [&](auto kernel, const auto &tB_) {
+        return launch_pdl_smem(kernel, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA0, tA1, tB_, a);
     };
     if (mode == 0) return go(k_grouped_gemm<0, false, false, false, true>, tB.a);
     if (mode == 3) return go(k_grouped_gemm<3>, tB.a);
@@ -1650,13 +1613,10 @@ cudaError_t launch_grouped_gemm_fp8(int mode, const moe_shape &s, const void *ac
     a.w_scale1 = w1_scale;
     a.row_scale = row_scale;
     a.row_addr = (mode == 1 && !comb) ? row_addr : nullptr;
-    static bool attr_done[4] = {false, false, false, false};
-    cudaError_t err;
-    auto setup = [&](const void *fn, int i) -> cudaError_t {
-        if (attr_done[i]) return cudaSuccess;
-        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-        if (e == cudaSuccess) attr_done[i] = true;
-        return e;
+    auto go = [&](auto kernel) {
+        const cudaError_t e =
+            launch_pdl_smem(kernel, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA0, tA1, tB, a);
+        return e == cudaSuccess ? cudaGetLastError() : e;
     };
     if (mode == 1 && comb) {
         a.src_token = comb->src_token;
@@ -1665,23 +1625,10 @@ cudaError_t launch_grouped_gemm_fp8(int mode, const moe_shape &s, const void *ac
         a.comb_out = (__nv_bfloat16 *)comb->out;
         a.comb_cnt = (int *)((char *)ws + L.combine_cnt);
         a.k = s.k;
-        if ((err = setup((const void *)k_grouped_gemm<1, false, true, true>, 3)) != cudaSuccess) return err;
-        err = launch_pdl(k_grouped_gemm<1, false, true, true>, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA0, tA1, tB, a);
-        if (err != cudaSuccess) return err;
-    } else if (gather) {
-        if ((err = setup((const void *)k_grouped_gemm<0, true, true>, 0)) != cudaSuccess) return err;
-        err = launch_pdl(k_grouped_gemm<0, true, true>, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA0, tA1, tB, a);
-        if (err != cudaSuccess) return err;
-    } else if (mode == 0) {
-        if ((err = setup((const void *)k_grouped_gemm<0, false, true>, 1)) != cudaSuccess) return err;
-        err = launch_pdl(k_grouped_gemm<0, false, true>, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA0, tA1, tB, a);
-        if (err != cudaSuccess) return err;
-    } else {
-        if ((err = setup((const void *)k_grouped_gemm<1, false, true>, 2)) != cudaSuccess) return err;
-        err = launch_pdl(k_grouped_gemm<1, false, true>, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA0, tA1, tB, a);
-        if (err != cudaSuccess) return err;
+        return go(k_grouped_gemm<1, false, true, true>);
     }
-    return cudaGetLastError();
+    if (gather) return go(k_grouped_gemm<0, true, true>);
+    return mode == 0 ? go(k_grouped_gemm<0, false, true>) : go(k_grouped_gemm<1, false, true>);
 }
 
 }  // namespace moe

@@ -519,12 +519,8 @@ __global__ void __launch_bounds__(256) k_route(RouteArgs a) {
 
 template <int TB, int EJ>
 cudaError_t launch_one(const RouteArgs &a, int smem_bytes, int tiles, cudaStream_t stream) {
-    static bool attr_done = false;
-    if (!attr_done) {
-        cudaError_t e = cudaFuncSetAttribute(k_route<TB, EJ>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteSmemMax);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    const cudaError_t e = allow_smem(k_route<TB, EJ>, kRouteSmemMax);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * a.cl));
     cfg.blockDim = dim3(256);

@@ -427,10 +427,7 @@ cudaError_t launch_wgrad(const moe_shape &s, int MA, int NB, const void *A, cons
     const int64_t total = (int64_t)s.E * a.m_tiles * a.n_tiles;
     if (total >= (1ll << 31) - num_sms) return cudaErrorInvalidValue;
     const int grid = total < num_sms ? (int)total : num_sms;
-    // set on every call: the attribute belongs to the current device
-    const cudaError_t e = cudaFuncSetAttribute(k_wgrad, cudaFuncAttributeMaxDynamicSharedMemorySize, kWSmem);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(k_wgrad, dim3(grid), dim3(kWThreads), kWSmem, stream, tA, tB0, tB1, tD0, tD1, a);
+    return launch_pdl_smem(k_wgrad, dim3(grid), dim3(kWThreads), kWSmem, stream, tA, tB0, tB1, tD0, tD1, a);
 }
 
 }  // namespace moe
