@@ -4,21 +4,28 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+#include <mutex>
+
 #include "common.cuh"
 
 namespace moe {
 namespace {
 
+// The driver's encoder: looked up by the first launch, by one thread where
+// several launch at once, and again after a look-up that failed.
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    return fn;
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> found{nullptr};
+    static std::mutex mutex;
+    if (auto fn = found.load(std::memory_order_acquire)) return fn;
+    std::lock_guard<std::mutex> lock(mutex);
+    if (auto fn = found.load(std::memory_order_relaxed)) return fn;
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+        found.store(reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p), std::memory_order_release);
+    return found.load(std::memory_order_relaxed);
 }
 
 // 2-D tensor map over a row-major [rows, cols] matrix of bf16 (or, with

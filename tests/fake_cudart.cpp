@@ -7,22 +7,29 @@
 #include <cuda.h>
 #include <cuda_runtime_api.h>
 
+#include <atomic>
+#include <chrono>
 #include <cstring>
 #include <map>
+#include <mutex>
+#include <thread>
 #include <utility>
 
 namespace {
 int g_device = 0;
 int g_launches = 0;
 std::map<std::pair<const void *, int>, size_t> g_limit;  // (kernel, device) -> bytes
-struct {
+std::mutex g_mutex;
+thread_local struct {
     dim3 grid, block;
     size_t smem;
     cudaStream_t stream;
 } g_config;
 char g_area[256];
+std::atomic<int> g_lookups{0}, g_failing_lookups{0};
 
 cudaError_t launch(const void *func, size_t smem) {
+    std::lock_guard<std::mutex> lock(g_mutex);
     const auto it = g_limit.find({func, g_device});
     if (smem > (it == g_limit.end() ? 48u * 1024u : it->second)) return cudaErrorInvalidValue;
     ++g_launches;
@@ -40,6 +47,8 @@ CUresult encode_tiled(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, co
 
 API void fake_set_device(int dev) { g_device = dev; }
 API int fake_launches() { return g_launches; }
+API int fake_lookups() { return g_lookups; }                        // of driver entry points
+API void fake_fail_lookups(int n) { g_failing_lookups = n; }  // the next n find nothing
 
 API cudaError_t cudaGetDevice(int *dev) {
     *dev = g_device;
@@ -50,6 +59,7 @@ API cudaError_t cudaDeviceGetAttribute(int *v, cudaDeviceAttr attr, int) {
     return cudaSuccess;
 }
 API cudaError_t cudaFuncSetAttribute(const void *func, cudaFuncAttribute attr, int value) {
+    std::lock_guard<std::mutex> lock(g_mutex);
     if (attr == cudaFuncAttributeMaxDynamicSharedMemorySize) g_limit[{func, g_device}] = (size_t)value;
     return cudaSuccess;
 }
@@ -81,7 +91,9 @@ API cudaError_t cudaGetSymbolAddress(void **p, const void *) {
 }
 API cudaError_t cudaGetDriverEntryPoint(const char *name, void **fn, unsigned long long,
                                         cudaDriverEntryPointQueryResult *q) {
-    const bool known = !std::strcmp(name, "cuTensorMapEncodeTiled");
+    ++g_lookups;
+    std::this_thread::sleep_for(std::chrono::milliseconds(200));  // long enough for another thread to arrive
+    const bool known = !std::strcmp(name, "cuTensorMapEncodeTiled") && g_failing_lookups-- <= 0;
     *fn = known ? (void *)encode_tiled : nullptr;
     if (q) *q = known ? cudaDriverEntryPointSuccess : cudaDriverEntryPointSymbolNotFound;
     return cudaSuccess;

@@ -6,6 +6,8 @@ import ctypes
 import glob
 import os
 import subprocess
+import sys
+import threading
 
 import pytest
 
@@ -47,11 +49,15 @@ def lib(tmp_path_factory):
     if len(objs) != len(moe_build.sources()):
         moe_build.build(force=True)
         objs = sorted(glob.glob(os.path.join(moe_build.HERE, "_build", "*.cu.o")))
-    out = str(tmp_path_factory.mktemp("fake") / "libmoe_fake.so")
+    path = str(tmp_path_factory.mktemp("fake") / "libmoe_fake.so")
     subprocess.check_call([os.environ.get("NVCC", "nvcc"), "-cudart", "none", "-shared", "-std=c++17",
-                           "-Xcompiler", "-fPIC", "-Xlinker", "-Bsymbolic", "-o", out,
+                           "-Xcompiler", "-fPIC", "-Xlinker", "-Bsymbolic", "-o", path,
                            os.path.join(HERE, "fake_cudart.cpp"), *objs])
-    fake, real = ctypes.CDLL(out), moe.load_library()
+    return load(path)
+
+
+def load(path):
+    fake, real = ctypes.CDLL(path), moe.load_library()
     for name in set(n.strip() for n in CALLS) | {"moe_forward", "moe_forward_checkpoint", "moe_backward"}:
         getattr(fake, name).argtypes = getattr(real, name).argtypes
     return fake
@@ -93,3 +99,34 @@ def test_the_fake_runtime_refuses_a_launch_above_the_limit(lib):
     lib.fake_set_device(1)
     assert launch(cfg, ctypes.byref(func), None) == 1
     lib.fake_set_device(0)
+
+
+def first_calls_of_two_threads(path):
+    """In a process of its own: the first GEMM launches of the process, two at once."""
+    lib = load(path)
+    s = moe.make_shape(64, 128, 256, 8, 2)
+    status = []
+    for name, n in (("moe_grouped_down", 5), ("moe_grouped_down_wgrad", 5)):
+        lib.fake_fail_lookups(1)
+        assert getattr(lib, name)(ctypes.byref(s), *[PTR] * n) != 0  # nothing found: refused, and looked up again
+        before = lib.fake_lookups()
+        start = threading.Barrier(2)
+
+        def call():
+            start.wait()
+            status.append(getattr(lib, name)(ctypes.byref(s), *[PTR] * n))
+
+        threads = [threading.Thread(target=call) for _ in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert lib.fake_lookups() - before == 1, "%s: %d threads looked the encoder up" % (
+            name, lib.fake_lookups() - before)
+    assert status == [0] * 4, status
+
+
+def test_first_calls_of_two_threads_look_the_encoder_up_once(lib):
+    code = "import test_launch_devices as t; t.first_calls_of_two_threads(%r)" % lib._name
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([HERE, os.path.dirname(HERE)]))
+    subprocess.run([sys.executable, "-c", code], check=True, env=env, timeout=120)
