@@ -1554,6 +1554,7 @@ cudaError_t launch_grouped_gemm_train(int mode, const moe_shape &s, const void *
     a.timeout_ns = timeout_ns;
     a.T = s.T;
     a.row_boxes = boxes;
+    a.stall_first_stage = (s.flags & MOE_FLAG_TEST_STALL_GEMM) ? 1 : 0;
     auto go = [&](auto kernel, const auto &tB_) {
         return launch_pdl_smem(kernel, dim3(num_sms), dim3(kThreads), kSmemBytes, stream, tA0, tA1, tB_, a);
     };

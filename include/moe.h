@@ -91,12 +91,15 @@ typedef enum {
                                    bounded wait expires and reports
                                    MOE_DEV_SCAN_TIMEOUT */
 #define MOE_FLAG_TEST_STALL_GEMM 0x20000000u /* test only: in moe_grouped_swiglu
-                                   (tiled form) the token-tile producer of
-                                   CTA 0 never loads its first stage, so the
-                                   MMA issuer's bounded wait expires; the
-                                   kernel reports MOE_DEV_GEMM_TIMEOUT, lets
-                                   its copies in flight land, frees its
-                                   tensor memory and returns */
+                                   (tiled form), moe_grouped_swiglu_checkpoint,
+                                   moe_grouped_down_backward and
+                                   moe_grouped_swiglu_backward the token-tile
+                                   producer of CTA 0 never loads its first
+                                   stage, so the MMA issuer's bounded wait
+                                   expires; the kernel reports
+                                   MOE_DEV_GEMM_TIMEOUT, lets its copies in
+                                   flight land, frees its tensor memory and
+                                   returns */
 
 typedef struct {
     int32_t T;      /* tokens */
