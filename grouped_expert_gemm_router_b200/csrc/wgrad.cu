@@ -74,6 +74,7 @@ struct WgradArgs {
     int n_tiles, n_blocks;  // the same of its columns, both outputs one after the other
     int blocks0;            // column blocks of the first output
     int MA;                 // rows of one expert's output
+    int stall_last_unit;    // test hook: CTA 0's producer never loads the first stage of its last unit
     unsigned long long timeout_ns;
 };
 
@@ -210,6 +211,16 @@ __global__ void __launch_bounds__(kWThreads, 1)
                     if (!mbar_wait_bounded(&empty[stage], ph ^ 1u, a.timeout_ns, s_abort)) {
                         ok = false;
                         break;
+                    }
+                    int next = i;
+                    if (a.stall_last_unit && kb == 0 && blockIdx.x == 0 && w_next(next) >= total) {
+                        // test hook: this stage is never loaded (no copy is in
+                        // flight for it), so the MMA issuer's wait expires
+                        if (++stage == kWStages) {
+                            stage = 0;
+                            ph ^= 1u;
+                        }
+                        continue;
                     }
                     int row, n;
                     w_block(U, kb, row, n);
@@ -423,6 +434,7 @@ cudaError_t launch_wgrad(const moe_shape &s, int MA, int NB, const void *A, cons
     a.n_blocks = (B1 ? 2 : 1) * a.blocks0;
     a.n_tiles = (a.n_blocks + 1) / 2;
     a.MA = MA;
+    a.stall_last_unit = (s.flags & MOE_FLAG_TEST_STALL_GEMM) ? 1 : 0;
     a.timeout_ns = timeout_ns;
     const int64_t total = (int64_t)s.E * a.m_tiles * a.n_tiles;
     if (total >= (1ll << 31) - num_sms) return cudaErrorInvalidValue;

@@ -99,7 +99,9 @@ typedef enum {
                                    expires; the kernel reports
                                    MOE_DEV_GEMM_TIMEOUT, lets its copies in
                                    flight land, frees its tensor memory and
-                                   returns */
+                                   returns; in the weight gradients the same
+                                   for the first stage of CTA 0's last unit,
+                                   while its earlier units are being stored */
 
 typedef struct {
     int32_t T;      /* tokens */

@@ -59,3 +59,54 @@ def test_wait_of_a_training_gemm_expires_and_reports(case, op):
     assert L.status() == 0
     for a, b in zip(_bits(got), _bits(ref)):
         assert torch.equal(a, b)
+
+
+def _gate_up_wgrad(L, shape, out):
+    moe.moe_grouped_swiglu_wgrad(shape, L.x_perm, L.dg, L.du, *out, L.ws)
+
+
+def _down_wgrad(L, shape, out):
+    moe.moe_grouped_down_wgrad(shape, L.h, L.dy, *out, L.ws)
+
+
+# every expert has rows, so that CTA 0's last unit has a stage to leave out: one unit per CTA (tiny), several units of
+# fewer blocks than the ring of three stages, and of more
+WGRAD = {"tiny": (64, 128, 256, 8, 2, None, "uniform"), "short": (1000, 1024, 2048, 16, 2, None, "uniform"),
+         "long": (3000, 1024, 2048, 12, 2, None, "uniform"), "capacity": (1500, 1024, 2048, 12, 2, 100, "uniform")}
+
+
+@pytest.mark.parametrize("op", [_gate_up_wgrad, _down_wgrad], ids=["gate_up", "down"])
+@pytest.mark.parametrize("case", list(WGRAD))
+def test_wait_of_a_weight_gradient_expires_and_reports(case, op):
+    """CTA 0's producer never loads the first stage of its last unit, while
+    the stores of the unit before may be in flight: only that unit's tile may
+    be missing."""
+    L = Layer(case, case=WGRAD[case])
+    assert int(L.counts.min()) > 0
+    L.h, L.dg, L.du, L.dy = L.rows(L.P, L.F), L.rows(L.P, L.F), L.rows(L.P, L.F), L.rows(L.P, L.H)
+
+    def buffers():
+        return [L.poison(L.E, L.F, L.H)] if op is _down_wgrad else [L.poison(L.E, L.H, L.F) for _ in range(2)]
+
+    ref = buffers()
+    op(L, L.shape, ref)
+    assert L.status() == 0
+    s = L.shape
+    stall = moe.make_shape(s.T, s.H, s.F, s.E, s.k, C=s.C, flags=s.flags | moe.MOE_FLAG_TEST_STALL_GEMM)
+    cut = buffers()
+    moe.moe_set_wait_timeout_ns(50_000_000)
+    try:
+        op(L, stall, cut)
+        status = moe.moe_read_status(L.ws, clear=True)
+    finally:
+        moe.moe_set_wait_timeout_ns(1_000_000_000)
+    assert status == moe.MOE_DEV_GEMM_TIMEOUT, hex(status)
+    missing = 0
+    for a, b in zip(_bits(cut), _bits(ref)):
+        missing += int((a != b).sum())
+    assert 0 < missing <= 256 * 256 * 2, "bytes of the unit that was left out: %d" % missing
+    got = buffers()
+    op(L, s, got)
+    assert L.status() == 0
+    for a, b in zip(_bits(got), _bits(ref)):
+        assert torch.equal(a, b)
