@@ -543,7 +543,9 @@ __device__ __forceinline__ void swiglu_backward_chunk(const GemmArgs &a, const U
             const float dh = __uint_as_float(r[j]);
             const float s = __fdividef(1.0f, 1.0f + __expf(-g[fi]));
             const float silu = g[fi] * s;
-            dg[j] = __float_as_uint(dh * u[fi] * fmaf(silu, 1.0f - s, s));
+            // u times the derivative (at most 1.1) first: dh u alone may
+            // overflow where the derivative makes it small, or zero
+            dg[j] = __float_as_uint(dh * (u[fi] * fmaf(silu, 1.0f - s, s)));
             du[j] = __float_as_uint(dh * silu);
             hh[j] = __float_as_uint(silu * u[fi]);
         }
