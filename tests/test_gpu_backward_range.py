@@ -77,3 +77,52 @@ def test_down_backward_far_from_zero(name, H):
               "dg")
         check(du[i], dh * g * s, up * (e_dh * (g * s).abs() + d * (e_silu + 2.0 ** -23 * (g * s).abs())), "du")
         check(h[i], g * s * u, up * (u.abs() * e_silu + 2.0 ** -23 * (g * s * u).abs()), "h")
+
+
+def _byte_of(f):
+    """Where feature f's code sits in a row."""
+    return f // 32 * 32 + 4 * (f % 8) + f % 32 // 8
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("name,case", [("ragged", (700, 256, 384, 4, 2, None, "uniform")),
+                                       ("few_rows", (40, 128, 128, 4, 4, None, "uniform")),
+                                       ("capacity", (200, 256, 256, 16, 4, 24, "skew"))])
+def test_checkpoint_of_one_non_finite_feature_in_a_block(name, case, value):
+    """One column of an expert's gate weights makes one feature of its rows
+    non-finite, one of its up weights another: those features' codes are NaN;
+    the scales, the other 31 codes of each block and h are those of the same
+    layer with these columns zero, bit for bit (a zero does not count for the
+    largest magnitude)."""
+    L = Layer(name, case=case)
+    e, fg, fu = L.E // 2, 37, 70
+    assert L.row_of[e].numel() > 0
+    L.w_gate[e, :, fg] = 0
+    L.w_up[e, :, fu] = 0
+
+    def run():
+        ck, h = moe.alloc_checkpoint(L.shape), L.poison(L.P, L.F)
+        for t in ck.values():
+            t.fill_(0xAB)
+        moe.moe_grouped_swiglu_checkpoint(L.shape, L.x_perm, L.w_gate, L.w_up, h, ck["g_q"], ck["u_q"], ck["scale"],
+                                          L.ws)
+        assert L.status() == 0
+        return ck, h.view(torch.int16)
+
+    ref, h_ref = run()
+    L.w_gate[e, 5, fg] = value
+    L.w_up[e, 9, fu] = value
+    got, h = run()
+    rows = L.row_of[e]
+    assert torch.equal(got["scale"], ref["scale"])
+    for q, f in (("g_q", fg), ("u_q", fu)):
+        assert ((got[q][rows, _byte_of(f)] & 0x7F) == 0x7F).all(), q
+        same = torch.ones(L.F, dtype=torch.bool, device="cuda")
+        same[_byte_of(f)] = False
+        assert torch.equal(got[q][:, same], ref[q][:, same]), q
+        others = torch.ones(L.P, dtype=torch.bool, device="cuda")
+        others[rows] = False
+        assert torch.equal(got[q][others], ref[q][others]), q
+    same = torch.ones(L.F, dtype=torch.bool, device="cuda")
+    same[[fg, fu]] = False
+    assert torch.equal(h[:, same], h_ref[:, same])
