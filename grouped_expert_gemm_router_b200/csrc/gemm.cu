@@ -511,8 +511,11 @@ __device__ __forceinline__ void unpack_e4m3x4(uint32_t w, float s, float (&v)[4]
 // Mode 3, the 16 rows x 32 features at unit column c0: dh from tensor memory
 // (fp32), gate and up from the checkpoint, dg, du and h stored as bf16 (the
 // gradients' and activations' type; the only roundings).  The sigmoid is
-// 1 / (1 + e^-g) with the fast exponential and division (a few 2^-22), not the
-// tanh of the forward epilogue: far negative g would lose its small value.
+// 1 / (1 + e^-g) with the fast exponential (2 + 1.16 |g| ulp) and division (2
+// ulp), not the tanh of the forward epilogue, whose error is absolute: off by
+// at most (5 + 1.16 |g|) 2^-23 of itself (2^-18.4 at g = -16, 2^-16.2 at -87,
+// against 2^-9 of the bf16 results); where e^-g passes 2^126, g < -87.3, it
+// may come out as 0 for what is below 2^-126.
 __device__ __forceinline__ void swiglu_backward_chunk(const GemmArgs &a, const Unit &U, uint32_t t0, int c0, int fbase,
                                                       int lane, uint8_t *stg) {
     uint32_t wg[4], wu[4], sc[4];
