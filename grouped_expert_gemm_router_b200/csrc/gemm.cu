@@ -130,10 +130,13 @@ constexpr int kWideMinK = 3584;
 // expert's weights stay in step and the units of a round cost the same (mode 4,
 // 4096 rows, 8 experts: 1016 -> 985 us; mode 3 there 590 -> 570; checkpoint
 // GEMM, 65536 rows, 128 experts: 470 -> 465).  Not for 128-feature units of
-// mode 3, whose short rest tiles hide behind the epilogue (312 -> 326).  Up to
-// this many tiles, where rounding to 16 cannot use the last tile up: n > 256
-// (nt - 1) rows leave it more than n/nt - 16 (nt - 1) - 16 > 0; beyond, the rest
-// is a small share.
+// mode 3, whose short rest tiles hide behind the epilogue (312 -> 326).  No
+// tile comes out empty: n rows in nt = ceil(n / 256) tiles are at most 256
+// high, and the first nt - 1 hold at most 256 (nt - 1) < n.  Up to this many
+// tiles: in a longer expert the rest tile is a small share, and equal heights
+// time the same (16384 rows, 7 experts of 10 tiles, H = F = 2048, back to
+// back: checkpoint GEMM 232 without and 231 with, mode 4 235 and 235; H 4096,
+// F 1408: mode 3 233 and 234).
 constexpr int kEvenTiles = 8;
 
 struct GemmArgs {
