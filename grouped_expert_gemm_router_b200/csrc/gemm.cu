@@ -120,9 +120,14 @@ constexpr uint32_t kTmemCols = 512;
 // Mode 3 (see its epilogue): 256-feature units from this reduction length up.
 // Their epilogue, the longest of all modes, is not overlapped, a fixed cost
 // per unit that the halved re-reading of the token rows pays back on long
-// reductions: K 4096 (4096 rows, 8 experts) 671 -> 628 us and K 3584 190 ->
-// 178 us, K 2560 457 -> 449 or 409 -> 424, K 2048 (65536 rows, 128 experts)
-// 328 -> 358 us back to back.
+// reductions.  Measured back to back, 128 -> 256 features: 65536 rows, 64
+// experts, F 768: K 2048 294 -> 288 us, 2304 319 -> 328, 2560 361 -> 352, 2816
+// 390 -> 377, 3328 476 -> 445, 3584 507 -> 458, 4096 580 -> 500; 65536 rows,
+// 128 experts, K 2048 328 -> 358; 4096 rows, 8 experts, F 14336, K 4096 671 ->
+// 628; but F 2048 there, one round of units either way: K 2048 70 -> 82, 3584
+// 110 -> 120, 4096 124 -> 131.  The rule looks at K alone; units of at most 128
+// rows, which hide their epilogue at either width, would gain at every length
+// (3200 rows, 32 experts, F 2816: K 2048 129 -> 104, 3328 190 -> 146).
 constexpr int kWideMinK = 3584;
 // Training GEMMs: the row tiles of an expert (uncapped: one run of rows) are
 // made equally high, in 16s, instead of 256, 256, ..., rest as the schedule has
