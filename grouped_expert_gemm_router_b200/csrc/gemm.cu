@@ -1199,8 +1199,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (MODE == 3) {
                 // dh stays in fp32 (its 256 KB are all of the register file, so
                 // it cannot wait there).  Units in one half of tensor memory
-                // overlap the next unit's MMAs; a unit in both halves hands
-                // back accumulator 0 while accumulator 1 is still read.
+                // overlap the next unit's MMAs.  A unit in both halves hands
+                // back accumulator 0 while accumulator 1 is still read, for a
+                // next unit that needs half 0 alone (one of at most 128 rows,
+                // or of an odd last feature block); one that needs both waits
+                // for accumulator 1 too, so its MMAs do not overlap.
 #pragma unroll 1
                 for (int acc = 0; acc < U.nacc; ++acc) {
 #pragma unroll 1
