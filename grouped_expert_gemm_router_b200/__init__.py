@@ -572,7 +572,12 @@ def backward_args(bufs: dict, rebuild_dispatch=False) -> MoeBackwardArgs:
 
 
 def moe_backward(shape, bufs: dict, ws, stream=None, args: MoeBackwardArgs | None = None, rebuild_dispatch=False):
-    """bufs: dict with the moe_backward_args field names -> tensors (or None)."""
+    """bufs: dict with the moe_backward_args field names -> tensors (or None).
+
+    bufs["dx"] becomes the experts' share of the input's gradient.  The
+    router's share is the caller's: with d = bufs["dlogits"] and w_r the
+    router's weights, x.float().t() @ d and d.sum(0) are the gradients of its
+    weights and bias, and dx.float() + d @ w_r.t() is the input's gradient."""
     a = args if args is not None else backward_args(bufs, rebuild_dispatch)
     _check(load_library().moe_backward(ctypes.byref(shape), ctypes.byref(a), _ptr(ws), _stream(stream)),
            "moe_backward")

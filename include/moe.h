@@ -752,7 +752,8 @@ typedef struct {
     void *dg, *du, *h;       /* [P,F] */
     void *dx_perm;           /* [P,H] (unused with dx == NULL) */
     /* results */
-    void *dx;                /* [T,H] bf16, or NULL: not wanted */
+    void *dx;                /* [T,H] bf16, or NULL: not wanted.  The experts' share
+                                alone: the layer input's gradient is dx + dlogits W_r^T */
     float *dtopk_w;          /* [T,k] */
     float *dlogits;          /* [T,E], or NULL: not wanted */
     void *dw_gate, *dw_up;   /* [E,H,F] bf16, or both NULL: not wanted */
@@ -762,9 +763,12 @@ typedef struct {
 /* The layer's backward pass on one stream: (moe_dispatch),
  * moe_combine_backward, moe_grouped_down_backward, moe_grouped_down_wgrad,
  * moe_grouped_swiglu_wgrad, moe_grouped_swiglu_backward, moe_gather_backward;
- * the steps whose results are not wanted are left out.  The router's own
- * weights get their gradient from dlogits: dW_r = x^T dlogits, dbias = its
- * column sums, and dx gains dlogits W_r^T; those products are the caller's. */
+ * the steps whose results are not wanted are left out.  The router's share is
+ * the caller's, three products of dlogits: dW_r = x^T dlogits, dbias = its
+ * column sums, and dx + dlogits W_r^T as the gradient of the layer's input: dx
+ * by itself is not that gradient (the share is as large as 0.4 of it in norm
+ * on random layers).  With the logits given by the caller
+ * (MOE_FLAG_LOGITS_IN), dlogits goes to whatever made them. */
 MOE_API moe_status moe_backward(const moe_shape *shape, const moe_backward_args *args, void *ws, void *stream);
 
 /* Upper bound, in nanoseconds, of every bounded device wait (default 1e9). */
