@@ -597,7 +597,9 @@ def alloc_checkpoint(shape: MoeShape, device="cuda"):
 
 def alloc_backward_buffers(shape: MoeShape, device="cuda"):
     """Intermediates and results of moe_backward (dx_perm shares dy's memory).
-    h is the forward buffer's name too: pass either."""
+    h is the forward buffer's name too.  Either buffer may be passed;
+    moe_backward writes the activations of the 8-bit codes into it, so the
+    forward pass's are lost from the one that is."""
     import torch
     T, H, F, E, k = shape.T, shape.H, shape.F, shape.E, shape.k
     P = moe_permuted_rows(shape)

@@ -665,7 +665,10 @@ MOE_API moe_status moe_ep_direct_quantize_h(const moe_shape *shape, int32_t G, c
  * max|v| <= 2^c over the block's finite values (1 for a block of zeros).  code
  * = the nearest e4m3 value of v / 2^(b-127), ties to even (relative error at
  * most 2^-4 down to 2^-13 of the block's largest value, absolute below); NaN
- * and infinite values are stored as NaN.  Inside a block of 32, byte
+ * and infinite values are stored as NaN.  (A finite |v| of 2^128 (1 - 2^-5) or
+ * more gets the code of 2^128, which reads back as infinite.)  On random layers
+ * the gradients that go through the codes differ from the float64 gradient by
+ * 3% in norm (dx, dw_gate, dw_up) and 4% (dw_down).  Inside a block of 32, byte
  * 4*(f%8) + f%32/8 is the code of feature f (the order in which the kernels
  * hold them).  Rows not filled are left unwritten, as in h and y.
  * ------------------------------------------------------------------------ */
@@ -677,7 +680,9 @@ MOE_API moe_status moe_dispatch(const moe_shape *shape, const int32_t *topk_idx,
 
 /* moe_grouped_swiglu (h is the same, bit for bit), writing the checkpoint too:
  * g_q, u_q [P,F] codes (16-byte aligned), scale [P,F/32,2] bytes (2-byte
- * aligned). */
+ * aligned).  In this h, as in moe_grouped_swiglu's, silu(g) comes from the
+ * hardware's tanh and is off by at most |g| 2^-12, measured inside bf16's
+ * rounding down to g = -6, 1% of silu(g) at -12, all of it at -16. */
 MOE_API moe_status moe_grouped_swiglu_checkpoint(const moe_shape *shape, const void *x_perm, const void *w_gate,
                                                  const void *w_up, void *h, void *g_q, void *u_q, void *scale,
                                                  void *ws, void *stream);
@@ -707,6 +712,10 @@ MOE_API moe_status moe_combine_backward(const moe_shape *shape, const void *dout
  *   dh = dy[r] . w_down[e][f,:]   (fp32, never written)
  *   dg = bf16( dh u s (1 + g (1 - s)) ),  du = bf16( dh g s ),
  *   h  = bf16( g s u ): the activations again, for moe_grouped_down_wgrad.
+ * s is within (5 + 1.16 |g|) 2^-23 of itself (below g = -87.3 within 2^-125).
+ * h is not the forward pass's: it has the codes' rounding of g and u and this
+ * s.  A caller that kept the forward pass's h can give that to
+ * moe_grouped_down_wgrad instead: dw_down is then within 0.3% in norm.
  * dg, du, h [P,F]; rows not filled are left unwritten. */
 MOE_API moe_status moe_grouped_down_backward(const moe_shape *shape, const void *dy, const void *w_down,
                                              const void *g_q, const void *u_q, const void *scale, void *dg, void *du,
@@ -749,7 +758,7 @@ typedef struct {
     int32_t *expert_counts, *expert_offsets, *src_token;
     /* intermediates; dx_perm may be the same buffer as dy */
     void *dy;                /* [P,H] */
-    void *dg, *du, *h;       /* [P,F] */
+    void *dg, *du, *h;       /* [P,F]; h is written: what it held is lost */
     void *dx_perm;           /* [P,H] (unused with dx == NULL) */
     /* results */
     void *dx;                /* [T,H] bf16, or NULL: not wanted.  The experts' share
