@@ -579,6 +579,9 @@ def moe_backward(shape, bufs: dict, ws, stream=None, args: MoeBackwardArgs | Non
     router's weights, x.float().t() @ d and d.sum(0) are the gradients of its
     weights and bias, and dx.float() + d @ w_r.t() is the input's gradient."""
     a = args if args is not None else backward_args(bufs, rebuild_dispatch)
+    if rebuild_dispatch and not a.rebuild_dispatch:  # prepared args without it: a copy that asks for it
+        a = MoeBackwardArgs.from_buffer_copy(a)
+        a.rebuild_dispatch = 1
     _check(load_library().moe_backward(ctypes.byref(shape), ctypes.byref(a), _ptr(ws), _stream(stream)),
            "moe_backward")
 
