@@ -31,13 +31,18 @@
 //   experts, capacity layout: checkpoint GEMM 117 us, 6.4 TB/s).  Many rows: a
 //   unit's K block moves its operands through shared memory twice (TMA writes,
 //   MMA reads) at 128 bytes a cycle, 1109 cycles for 206 rows x 256 features
-//   against 820 of MMA, and the units together take what L2 delivers, 13 TB/s
-//   (65536 rows, 128 experts, H 2048, F 768: mode 3 268 us, checkpoint GEMM
-//   409 us; 4096 rows, 8 experts, H 4096, F 14336: mode 4 844 us, where three
-//   rounds of 107 CTAs leave a third of the SM time idle; handing units out
-//   from a counter, or in smaller pieces, evens that out and is slower: CTAs
-//   that run the row tiles of one expert side by side share its weights in L2).
-//   At the 1000 W cap, back to back, 323, 478 and 995 us.
+//   against 820 of MMA.  What comes on top (single passes): in mode 3 the
+//   epilogue, an exponential, a division and three outputs per value, and each
+//   dy row read once per 128 features (65536 rows, 128 experts, H 2048, F 768:
+//   268 us, L2 to the SMs at 13 TB/s, of 21 that loads alone reach); in the
+//   checkpoint GEMM the codes, stored while the accumulators are held (there
+//   with loads skewed by alpha 1 409-433 us, 387 without the codes); in mode 4
+//   whole rounds (4096 rows, 8 experts, H 4096, F 14336: 844-909 us, three
+//   rounds of 107 CTAs, a third of the SM time idle; handing units out from a
+//   counter, or in smaller pieces, evens that out and is slower: CTAs that run
+//   the row tiles of one expert side by side share its weights in L2).  Back to
+//   back the 1000 W cap lowers the clock: 323-366, 478-503 and 973-1032 us on
+//   several GPUs.
 //
 // Design (B200 first, not the page's Triton kernel):
 // - Swap-AB.  The MMA computes D[feature, row] = W^T[feature, k] * X^T[k, row]:
@@ -124,8 +129,8 @@ constexpr uint32_t kTmemCols = 512;
 // experts, F 768: K 2048 294 -> 288 us, 2304 319 -> 328, 2560 361 -> 352, 2816
 // 390 -> 377, 3328 476 -> 445, 3584 507 -> 458, 4096 580 -> 500; 65536 rows,
 // 128 experts, K 2048 328 -> 358; 4096 rows, 8 experts, F 14336, K 4096 671 ->
-// 628; but F 2048 there, one round of units either way: K 2048 70 -> 82, 3584
-// 110 -> 120, 4096 124 -> 131.  The rule looks at K alone; units of at most 128
+// 628; but F 2048 there, 168 units in place of 336: K 2048 70 -> 82, 3584 110
+// -> 120, 4096 124 -> 131.  The rule looks at K alone; units of at most 128
 // rows, which hide their epilogue at either width, would gain at every length
 // (3200 rows, 32 experts, F 2816: K 2048 129 -> 104, 3328 190 -> 146).
 constexpr int kWideMinK = 3584;

@@ -32,14 +32,18 @@
 //   run.
 // - Every wait is bounded as in the forward GEMMs (MOE_DEV_GEMM_TIMEOUT).
 //
-// What bounds it: few rows per expert, the bytes written (T 512, 8 experts,
-// 4096 x 14336: 180 us alone, 5.3 TB/s; a plain fill of memory runs at 3.9);
-// many rows, shared memory, 64 KB of TMA writes and 96 KB of MMA reads per 64
-// rows at 128 bytes a cycle, 1280 cycles for 1024 of MMA (65536 rows, 128
-// experts, gate and up of 2048 x 768: 378 us, 1.09 PFLOP/s; 16384 rows, 8
-// experts, 4096 x 2560: 453 us, 1.52 PFLOP/s).  Pairs of CTAs on 512 x 256
-// outputs move a quarter less and were no faster (404-440 and 495 us): their
-// MMAs run at 80% of the nominal rate, and the GPU is at its power cap.
+// What bounds it.  Few rows per expert: the bytes written, with as many loaded
+// to make them (T 512, 8 experts, 4096 x 14336, two K blocks per unit: 180-199
+// us alone, 0.94 GB written at 4.7-5.3 TB/s and 2.26 GB through L2; stores
+// alone reach 6.2-6.9 TB/s, loads from L2 alone 21).  Many rows: inside a unit
+// shared memory, 64 KB of TMA writes and 96 KB of MMA reads per 64 rows at 128
+// bytes a cycle, 1280 cycles for 1024 of MMA; around it the drain, which no MMA
+// overlaps, because the two accumulators are all of tensor memory (65536 rows,
+// 128 experts, gate and up of 2048 x 768, eight K blocks per unit: 378-398 us,
+// 1.04-1.09 PFLOP/s, the tensor pipe busy 59%; 16384 rows, 8 experts, 4096 x
+// 2560: 453 us, 1.52 PFLOP/s).  Pairs of CTAs on 512 x 256 outputs move a
+// quarter less and were no faster (404-440 and 495 us): their MMAs run at 80%
+// of the nominal rate.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
